@@ -22,6 +22,12 @@ W4_OK, W4_ERR_INVALID_ARG, W4_ERR_UNSUPPORTED, W4_ERR_CUDA, W4_ERR_TIMEOUT, W4_E
 W4_F16, W4_BF16, W4_F32 = 0, 1, 2
 W4_FP4_NVFP4, W4_FP4_MXFP4 = 0, 1
 FP4_BLOCK = {W4_FP4_NVFP4: 16, W4_FP4_MXFP4: 32}
+W4_ACT_NONE, W4_ACT_RELU, W4_ACT_SILU, W4_ACT_GELU, W4_ACT_GELU_TANH = range(5)
+W4_ROPE_PLAIN, W4_ROPE_LINEAR, W4_ROPE_BASE, W4_ROPE_BANDS, W4_ROPE_RAMP = range(5)
+_ACTIVATIONS = {None: W4_ACT_NONE, "none": W4_ACT_NONE, "relu": W4_ACT_RELU, "silu": W4_ACT_SILU,
+                "gelu": W4_ACT_GELU, "gelu_tanh": W4_ACT_GELU_TANH}
+_ROPE_SCALINGS = {None: W4_ROPE_PLAIN, "plain": W4_ROPE_PLAIN, "linear": W4_ROPE_LINEAR,
+                  "base": W4_ROPE_BASE, "bands": W4_ROPE_BANDS, "ramp": W4_ROPE_RAMP}
 
 _lib = None
 _lib_lock = threading.Lock()
@@ -93,6 +99,18 @@ def lib():
         L.w4a16_gemm_chain.restype = st
         L.w4a16_chain_workspace_bytes.argtypes = [i64]
         L.w4a16_chain_workspace_bytes.restype = sz
+        L.w4a16_gemm_epi.argtypes = [vp, st, i64, i64, i64, vp, vp, vp, vp, vp, i32, vp,
+                                     ctypes.POINTER(Epilogue), vp, st, vp, sz, vp]
+        L.w4a16_gemm_epi.restype = st
+        f32, f64 = ctypes.c_float, ctypes.c_double
+        L.w4_rope.argtypes = [vp, st, i64, i32, i32, i64, i64, vp, vp, i32, f32, i32, vp, i64, i64, vp]
+        L.w4_rope.restype = st
+        L.w4_rope_freqs.argtypes = [i32, f64, st, f64, f64, f64, f64, ctypes.POINTER(f64), ctypes.POINTER(f32)]
+        L.w4_rope_freqs.restype = st
+        L.w4_prompt_attention.argtypes = [ctypes.POINTER(Attention), st, vp, sz, vp]
+        L.w4_prompt_attention.restype = st
+        L.w4_prompt_attention_workspace_bytes.argtypes = [i32, i32, i32, i32, i64, i64]
+        L.w4_prompt_attention_workspace_bytes.restype = sz
         _lib = L
     return _lib
 
@@ -103,6 +121,23 @@ class ChainLayer(ctypes.Structure):
                 ("scales", ctypes.c_void_p), ("zeros", ctypes.c_void_p), ("s_inv", ctypes.c_void_p),
                 ("Y", ctypes.c_void_p), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
                 ("group_size", ctypes.c_int32)]
+
+
+class Epilogue(ctypes.Structure):
+    """w4_epilogue of include/w4a16.h."""
+    _fields_ = [("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("ldr", ctypes.c_int64),
+                ("ldy", ctypes.c_int64), ("bias_dtype", ctypes.c_int), ("residual_dtype", ctypes.c_int),
+                ("activation", ctypes.c_int), ("gated", ctypes.c_int32)]
+
+
+class Attention(ctypes.Structure):
+    """w4_attention of include/w4a16.h."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("Q", "K", "V", "O", "lse", "cu_seqlens_q", "cu_seqlens_k")]
+                + [(n, ctypes.c_int64) for n in ("q_tokens", "k_tokens", "q_token_stride", "q_head_stride",
+                                                 "k_token_stride", "k_head_stride", "v_token_stride",
+                                                 "v_head_stride", "o_token_stride", "o_head_stride")]
+                + [(n, ctypes.c_int32) for n in ("batch", "heads", "kv_heads", "head_dim")]
+                + [("scale", ctypes.c_float), ("causal", ctypes.c_int32)])
 
 
 # ---------------------------------------------------------------- marshalling helpers
@@ -601,3 +636,218 @@ def w4_selftest_expired_wait(stream=None):
     torch = _torch()
     dev = torch.device("cuda", torch.cuda.current_device())
     _check(lib().w4_selftest_expired_wait(_stream_handle(stream, dev)), "w4_selftest_expired_wait")
+
+
+# ---------------------------------------------------------------- around the projections
+def gated_rows(F, device=None):
+    """Row order of gated weights for w4a16_gemm_epi(gated=True): an index into the rows of
+    [gate; up] ([2F, K], F a multiple of 8) that puts them in alternating blocks of 8, e.g.
+    w4_quantize_pack(torch.cat([W_gate, W_up])[gated_rows(F)]); a bias is ordered the same."""
+    torch = _torch()
+    if F % 8 != 0:
+        raise ValueError(f"F = {F} must be a multiple of 8")
+    f = torch.arange(F, device=device).view(-1, 1, 8)
+    return torch.cat([f, f + F], 1).reshape(-1)
+
+
+def _rows_of(t, name, dtypes, shape, dev):
+    """A matrix of the given shape whose elements are contiguous within rows (rows may be
+    further apart); returns its row stride."""
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.device != dev:
+        raise ValueError("tensors are on different devices")
+    if t.shape[0] <= 1:
+        if t.shape[1] > 1 and t.stride(1) != 1:
+            raise ValueError(f"{name}: elements of a row must be contiguous")
+        return t.shape[1]
+    if (t.shape[1] > 1 and t.stride(1) != 1) or t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name}: elements of a row must be contiguous, and rows must not overlap")
+    return t.stride(0)
+
+
+def w4a16_gemm_epi(X, qweight, scales, zeros, group_size=128, bias=None, activation=None, gated=False,
+                   residual=None, g_idx=None, s_inv=None, out_dtype=None, Y=None, workspace=None,
+                   stream=None, perm=None):
+    """w4a16_gemm with an epilogue in the same kernel, applied in fp32 before the one rounding:
+
+        t = (X * s_inv) @ dequant(...)^T + bias
+        Y = act(t) + residual                        [M, N]
+        Y = act(t_gate) * t_up + residual            [M, N/2], gated
+
+    activation: None, "relu", "silu", "gelu" (erf) or "gelu_tanh".  gated: the packed rows (and
+    bias) are in the order of gated_rows().  residual and Y may be row-strided views (rows on
+    16-byte boundaries); residual may be Y itself.  Workspace rules as w4a16_gemm."""
+    torch = _torch()
+    M, K, N = _gemm_args(X, qweight, scales, zeros, group_size, g_idx, s_inv, None, perm)
+    if perm is not None and g_idx is not None:
+        raise ValueError("pass g_idx or perm, not both")
+    act = _ACTIVATIONS.get(activation)
+    if act is None:
+        raise ValueError(f"unknown activation {activation!r} ({', '.join(k for k in _ACTIVATIONS if k)})")
+    floats = _dtypes()[:3]
+    if bias is not None and (bias.dtype not in floats or bias.numel() != N):
+        _expect(bias, "bias", floats, numel=N)
+    dev = _need_cuda(X, qweight, scales, zeros, g_idx, s_inv, bias, workspace, perm)
+    n_out = N // 2 if gated else N
+    if Y is None:
+        Y = torch.empty(M, n_out, dtype=out_dtype or X.dtype, device=dev)
+        ldy = n_out
+    else:
+        if out_dtype is not None and out_dtype != Y.dtype:
+            raise TypeError(f"Y is {Y.dtype}, out_dtype {out_dtype}")
+        ldy = _rows_of(Y, "Y", floats, (M, n_out), dev)
+    e = Epilogue()
+    e.ldy = ldy
+    e.activation = act
+    e.gated = 1 if gated else 0
+    if bias is not None:
+        e.bias = bias.data_ptr()
+        e.bias_dtype = _dtype_code(bias.dtype)
+    if residual is not None:
+        e.ldr = _rows_of(residual, "residual", floats, (M, n_out), dev)
+        e.residual = residual.data_ptr()
+        e.residual_dtype = _dtype_code(residual.dtype)
+    with _DeviceGuard(dev):
+        L = lib()
+        if workspace is None and M > 0:
+            need = (L.w4a16_workspace_bytes if perm is None else L.w4a16_workspace_bytes_perm)(M, N, K, int(group_size))
+            if need > 0:
+                workspace = workspace_for(dev, need)
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        st = L.w4a16_gemm_epi(_ptr(X), _dtype_code(X.dtype), M, N, K, _ptr(qweight), _ptr(scales), _ptr(zeros),
+                              _ptr(g_idx), _ptr(perm), int(group_size), _ptr(s_inv), e, _ptr(Y),
+                              _dtype_code(Y.dtype), _ptr(workspace), ws_bytes, _stream_handle(stream, dev))
+    _check(st, "w4a16_gemm_epi")
+    return Y
+
+
+def _heads_of(t, name, dev=None, dtype=None, shape=None):
+    """A [tokens, heads, head_dim] CUDA tensor (a view with contiguous head elements)."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim], not of shape {tuple(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError("all tensors must be CUDA tensors (there is no CPU path)")
+    if dev is not None and t.device != dev:
+        raise ValueError("tensors are on different devices")
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name}: elements of a head must be contiguous")
+    return t.stride(0), t.stride(1)
+
+
+def w4_rope_freqs(rot_dim, theta=10000.0, scaling=None, factor=1.0, context=8192, lo=1.0, hi=4.0, device=None):
+    """(inv_freq float64 [rot_dim/2], mscale) for w4_rope: theta^(-2i/rot_dim), stretched for
+    contexts longer than `context` by scaling = "linear", "base", "bands" or "ramp" (see
+    include/w4a16.h).  Computed on the host and copied to `device` (default: the current CUDA
+    device): once per model."""
+    torch = _torch()
+    code = _ROPE_SCALINGS.get(scaling)
+    if code is None:
+        raise ValueError(f"unknown scaling {scaling!r} ({', '.join(k for k in _ROPE_SCALINGS if k)})")
+    rot_dim = int(rot_dim)
+    out = (ctypes.c_double * max(1, rot_dim // 2))()
+    mscale = ctypes.c_float()
+    _check(lib().w4_rope_freqs(rot_dim, float(theta), code, float(factor), float(context), float(lo), float(hi),
+                               out, ctypes.byref(mscale)), "w4_rope_freqs")
+    freqs = torch.tensor(out[:], dtype=torch.float64)
+    return freqs.to(device if device is not None else "cuda"), mscale.value
+
+
+def w4_rope(X, positions, inv_freq, interleaved=False, mscale=1.0, Y=None, stream=None):
+    """Rotary positions on X [tokens, heads, head_dim] (fp16, bf16 or fp32; any view with
+    contiguous head elements, e.g. the query and key heads of a fused projection's output):
+    the first 2 * len(inv_freq) elements of each head are rotated by positions[t] *
+    inv_freq[i], as pairs (i, i + len(inv_freq)) or, interleaved, (2i, 2i+1).  positions int32
+    [tokens], inv_freq float64.  Y=X rotates in place; without Y a new tensor is returned."""
+    torch = _torch()
+    sx = _heads_of(X, "X")
+    dev = X.device
+    T, H, D = X.shape
+    _expect(positions, "positions", (torch.int32,), shape=(T,))
+    _expect(inv_freq, "inv_freq", (torch.float64,))
+    if inv_freq.dim() != 1 or 2 * inv_freq.shape[0] > D or inv_freq.shape[0] == 0:
+        raise ValueError(f"inv_freq must hold 1 .. {D // 2} frequencies, not {tuple(inv_freq.shape)}")
+    _need_cuda(positions, inv_freq)
+    if positions.device != dev or inv_freq.device != dev:
+        raise ValueError("tensors are on different devices")
+    if Y is None:
+        Y = torch.empty(T, H, D, dtype=X.dtype, device=dev)
+        sy = (H * D, D)
+    else:
+        sy = _heads_of(Y, "Y", dev, X.dtype, X.shape)
+    with _DeviceGuard(dev):
+        st = lib().w4_rope(X.data_ptr(), _dtype_code(X.dtype), T, H, D, sx[0], sx[1], positions.data_ptr(),
+                           inv_freq.data_ptr(), 2 * inv_freq.shape[0], float(mscale), 1 if interleaved else 0,
+                           Y.data_ptr(), sy[0], sy[1], _stream_handle(stream, dev))
+    _check(st, "w4_rope")
+    return Y
+
+
+def w4_prompt_attention_workspace_bytes(batch, heads, kv_heads, head_dim, q_tokens, k_tokens):
+    return int(lib().w4_prompt_attention_workspace_bytes(int(batch), int(heads), int(kv_heads), int(head_dim),
+                                                         int(q_tokens), int(k_tokens)))
+
+
+def w4_prompt_attention(Q, K, V, cu_seqlens=None, cu_seqlens_k=None, causal=True, scale=None, O=None,
+                        return_lse=False, workspace=None, stream=None):
+    """Softmax attention of packed sequences: Q [q_tokens, heads, head_dim], K and V
+    [k_tokens, kv_heads, head_dim] (fp16 or bf16; views with contiguous head elements and
+    strides of multiples of 8, e.g. slices of a fused projection's output), heads a multiple
+    of kv_heads.  cu_seqlens int32 [batch+1]: the sequences' bounds in Q, cu_seqlens_k those in
+    K and V when keys precede the queries; without them one sequence.  causal aligns the last
+    query with the last key.  scale defaults to head_dim^-0.5.
+
+    Returns O [q_tokens, heads, head_dim] (rows behind the last sequence are not written), and
+    with return_lse also lse float32 [q_tokens, heads].
+
+    Where a call needs scratch (w4_prompt_attention_workspace_bytes) and passes none, it is
+    allocated on the current stream; pass `workspace` when `stream` is another one."""
+    torch = _torch()
+    sq, sk, sv = _heads_of(Q, "Q"), _heads_of(K, "K"), _heads_of(V, "V")
+    dt, dev = Q.dtype, Q.device
+    if dt is not torch.float16 and dt is not torch.bfloat16:
+        raise TypeError(f"Q must be torch.float16 or torch.bfloat16, not {dt}")
+    if K.dtype != dt or V.dtype != dt:
+        raise TypeError("Q, K and V must have one dtype")
+    Tq, H, D = Q.shape
+    Tk, Hk = K.shape[0], K.shape[1]
+    if K.shape != V.shape or K.shape[2] != D:
+        raise ValueError(f"K and V must be [k_tokens, kv_heads, {D}], not {tuple(K.shape)} and {tuple(V.shape)}")
+    if K.device != dev or V.device != dev:
+        raise ValueError("tensors are on different devices")
+    batch = 1
+    for cu, name in ((cu_seqlens, "cu_seqlens"), (cu_seqlens_k, "cu_seqlens_k")):
+        if cu is None:
+            continue
+        if cu.dtype is not torch.int32:
+            raise TypeError(f"{name} must be torch.int32, not {cu.dtype}")
+        if cu.dim() != 1 or cu.shape[0] < 1 or not cu.is_contiguous() or cu.device != dev:
+            raise ValueError(f"{name} must be a contiguous vector of batch+1 bounds on {dev}")
+        batch = cu.shape[0] - 1
+    if cu_seqlens_k is not None and (cu_seqlens is None or cu_seqlens.shape != cu_seqlens_k.shape):
+        raise ValueError("cu_seqlens_k needs a cu_seqlens of the same length")
+    if O is None:
+        O = torch.empty(Tq, H, D, dtype=dt, device=dev)
+        so = (H * D, D)
+    else:
+        so = _heads_of(O, "O", dev, dt, Q.shape)
+    lse = torch.empty(Tq, H, dtype=torch.float32, device=dev) if return_lse else None
+    a = Attention(Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), _ptr(lse), _ptr(cu_seqlens),
+                  _ptr(cu_seqlens_k), Tq, Tk, sq[0], sq[1], sk[0], sk[1], sv[0], sv[1], so[0], so[1],
+                  batch, H, Hk, D, D ** -0.5 if scale is None else float(scale), 1 if causal else 0)
+    with _DeviceGuard(dev):
+        L = lib()
+        if workspace is None:
+            need = L.w4_prompt_attention_workspace_bytes(batch, H, Hk, D, Tq, Tk)
+            if need > 0:
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        st = L.w4_prompt_attention(a, _dtype_code(dt), _ptr(workspace), ws_bytes, _stream_handle(stream, dev))
+    _check(st, "w4_prompt_attention")
+    return (O, lse) if return_lse else O

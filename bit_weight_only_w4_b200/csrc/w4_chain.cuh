@@ -253,11 +253,11 @@ __global__ void __launch_bounds__(w4d::Cfg<1>::threads, 1)
             }
             combine_sets<1, TPW>(xchg, set, t0, L, acc);
             if (pe == (band + 1) * p.KU && ps > band * p.KU) continue;   // completed below
-            if (set == 0 && !aborted) flush_part<1, TPW>(p, band, pe, cta, t0, L, acc);
+            if (set == 0 && !aborted) flush_part<1, TPW>(p, w4e::Epilogue{}, band, pe, cta, t0, L, acc);
             zero_acc<1, TPW>(acc);
         }
         if (u0 > it.b0 * p.KU && u1 >= (it.b0 + 1) * p.KU)
-            complete_band<1, TPW>(p, smem, xchg, s_abort, it.b0, cta, set, t0, L, aborted, acc);
+            complete_band<1, TPW>(p, w4e::Epilogue{}, smem, xchg, s_abort, it.b0, cta, set, t0, L, aborted, acc);
     }
     // the last layer is done everywhere once every CTA has arrived; the last arrival
     // zeroes the counter for the next launch (nothing reads it after that)

@@ -41,6 +41,7 @@
 //               (deterministic, no atomics).
 #pragma once
 #include "w4_common.cuh"
+#include "w4_epilogue.cuh"
 #include "w4_fp4.cuh"
 
 namespace w4d {
@@ -159,12 +160,13 @@ W4_DEV void stage_atoms(const DecodeParams& p, int band, int ps, int pe, int st,
     na = min(2 * nu, p.KA - a0);
 }
 
-W4_DEV void store_out(const DecodeParams& p, int m, int n, float v) {
-    const size_t idx = (size_t)m * p.N + n;
+W4_DEV void store_elem(const DecodeParams& p, size_t idx, float v) {
     if (p.out_dtype == 2) reinterpret_cast<float*>(p.Y)[idx] = v;
     else if (p.out_dtype == 1) reinterpret_cast<__nv_bfloat16*>(p.Y)[idx] = __float2bfloat16_rn(v);
     else reinterpret_cast<__half*>(p.Y)[idx] = __float2half_rn(v);
 }
+
+W4_DEV void store_out(const DecodeParams& p, int m, int n, float v) { store_elem(p, (size_t)m * p.N + n, v); }
 
 // Shared-memory loads through pointers derived from the dynamic shared array (the
 // compiler keeps them after the mbarrier waits, whose asm clobbers memory, and is free to
@@ -216,9 +218,20 @@ W4_DEV bool slot_wait(const unsigned long long* a, float& v) {
 // a[2] = row r0 cols c+8,c+9; a[3] = row r1 cols c+8,c+9, each element o + m*q exactly:
 //   fp16: rows r0 (nibbles 0,2,4,6): 1024 + q;  rows r1 (nibbles 1,3,5,7): 1024 + 16 q;
 //   bf16: every element 128 + q.
-template <bool BF16>
+// SUB (fp16, the products with an epilogue): the nibbles alone, read as subnormal fp16
+// numbers: rows r0 q 2^-24, rows r1 q 2^-20, exactly (the tensor cores multiply subnormal
+// fp16 operands exactly), at the same instruction count.  The biased codes make partial
+// sums about 200 times the result, and their fp32 rounding is then as large as an fp16
+// output's (2e-4 relative); without the bias it is below 1e-5.
+template <bool BF16, bool SUB = false>
 W4_DEV void unpack_biased(uint32_t w, uint32_t (&a)[4]) {
-    if constexpr (!BF16) {
+    if constexpr (SUB) {
+        const uint32_t w8 = w >> 8;
+        a[0] = w & 0x000F000Fu;
+        a[1] = w & 0x00F000F0u;
+        a[2] = w8 & 0x000F000Fu;
+        a[3] = w8 & 0x00F000F0u;
+    } else if constexpr (!BF16) {
         const uint32_t w8 = w >> 8;
         a[0] = and_or(w, 0x000F000Fu, 0x64006400u);
         a[1] = and_or(w, 0x00F000F0u, 0x64006400u);
@@ -238,12 +251,17 @@ struct RowFold {
     float scp, bz;
 };
 
-template <bool BF16, bool HI>
+template <bool BF16, bool HI, bool SUB = false>
 W4_DEV RowFold row_fold(uint32_t sc_bits, uint32_t z_bits) {
     const float sc = __half2float(__ushort_as_half((unsigned short)sc_bits));
     const float z = __half2float(__ushort_as_half((unsigned short)z_bits));
     RowFold f;
-    if constexpr (BF16) {
+    if constexpr (SUB) {
+        // products of q 2^-24 (rows r0) or q 2^-20 (rows r1); the sums keep that power of two
+        // until store_rows_epi
+        f.scp = sc;
+        f.bz = -z * (HI ? 1.0f / 1048576.0f : 1.0f / 16777216.0f);
+    } else if constexpr (BF16) {
         f.scp = sc;
         f.bz = -(128.0f + z);
     } else if constexpr (HI) {
@@ -346,7 +364,7 @@ W4_DEV void mma_16816_z(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint
 }
 
 // One 16-deep step of TPW row tiles against NT token tiles; FIRST starts the partial sums.
-template <int NT, int TPW, bool BF16, bool FIRST>
+template <int NT, int TPW, bool BF16, bool FIRST, bool SUB = false>
 W4_DEV void mma_step(const uint32_t (&wj)[TPW], const unsigned char* xa, int xl, int xh, int lane, int j,
                      float (&c)[TPW][NT][4]) {
     uint32_t b0[NT], b1[NT];
@@ -359,7 +377,7 @@ W4_DEV void mma_step(const uint32_t (&wj)[TPW], const unsigned char* xa, int xl,
 #pragma unroll
     for (int tt = 0; tt < TPW; ++tt) {
         uint32_t af[4];
-        unpack_biased<BF16>(wj[tt], af);
+        unpack_biased<BF16, SUB>(wj[tt], af);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             if constexpr (FIRST) mma_16816_z<BF16>(c[tt][nt], af, b0[nt], b1[nt]);
@@ -378,7 +396,7 @@ W4_DEV void load_sums(const unsigned char* sx, int seg, int sstride, const Lane&
 // acc += sc' * (c + bz * S) per element, with the row's {sc', bz} from its staged fp16
 // scale and zero point and S, per token tile, the activation sums of tokens 8nt+2q and
 // 8nt+2q+1 over the folded channels.
-template <int NT, int TPW, bool BF16>
+template <int NT, int TPW, bool BF16, bool SUB = false>
 W4_DEV void fold(const StageView& v, const Lane& L, int t0, int grow, const float2 (&S)[NT],
                  const float (&c)[TPW][NT][4], float (&acc)[TPW][NT][4]) {
 #pragma unroll
@@ -387,8 +405,8 @@ W4_DEV void fold(const StageView& v, const Lane& L, int t0, int grow, const floa
         const uint32_t sc0 = ld_u16(v.sc + o0), sc1 = ld_u16(v.sc + o1);
         const uint32_t z0 = v.zr ? ld_u16(v.zr + o0) : 0x4800u;   // symmetric: z = 8
         const uint32_t z1 = v.zr ? ld_u16(v.zr + o1) : 0x4800u;
-        const RowFold f0 = row_fold<BF16, false>(sc0, z0);
-        const RowFold f1 = row_fold<BF16, true>(sc1, z1);
+        const RowFold f0 = row_fold<BF16, false, SUB>(sc0, z0);
+        const RowFold f1 = row_fold<BF16, true, SUB>(sc1, z1);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             acc[tt][nt][0] = fmaf(f0.scp, fmaf(f0.bz, S[nt].x, c[tt][nt][0]), acc[tt][nt][0]);
@@ -413,7 +431,7 @@ W4_DEV void zero_acc(float (&c)[TPW][NT][4]) {
 }
 
 // Consume atoms [ab, ae) of the stage for row tiles t0..t0+TPW-1 (contiguous groups).
-template <int NT, int TPW, bool BF16, int MODE>
+template <int NT, int TPW, bool BF16, int MODE, bool SUB = false>
 W4_DEV void consume(const StageView& v, const Lane& L, int t0, int ab, int ae, int g,
                     float (&acc)[TPW][NT][4]) {
     const unsigned char* wl = v.codes + t0 * 512 + L.lane * 16;
@@ -477,7 +495,7 @@ W4_DEV void consume(const StageView& v, const Lane& L, int t0, int ab, int ae, i
 #pragma unroll
                     for (int tt = 0; tt < TPW; ++tt) {
                         uint32_t af[4];
-                        unpack_biased<BF16>(word_j<TPW>(w[aa][tt], j), af);
+                        unpack_biased<BF16, SUB>(word_j<TPW>(w[aa][tt], j), af);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             float (&d)[4] = (CH == 2 && (st & 1)) ? c2[tt][nt] : c[tt][nt];
@@ -499,8 +517,8 @@ W4_DEV void consume(const StageView& v, const Lane& L, int t0, int ab, int ae, i
             for (int nt = 0; nt < NT; ++nt) S[nt] = ld_f2(sxp + (pr * v.sstride + 8 * nt) * 4);
 #pragma unroll
             for (int tt = 0; tt < TPW; ++tt) {
-                const RowFold f0 = row_fold<BF16, false>(md[tt][0], md[tt][2]);
-                const RowFold f1 = row_fold<BF16, true>(md[tt][1], md[tt][3]);
+                const RowFold f0 = row_fold<BF16, false, SUB>(md[tt][0], md[tt][2]);
+                const RowFold f1 = row_fold<BF16, true, SUB>(md[tt][1], md[tt][3]);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     acc[tt][nt][0] = fmaf(f0.scp, fmaf(f0.bz, S[nt].x, c[tt][nt][0]), acc[tt][nt][0]);
@@ -533,12 +551,12 @@ W4_DEV void consume(const StageView& v, const Lane& L, int t0, int ab, int ae, i
                 uint32_t wj[TPW];
 #pragma unroll
                 for (int tt = 0; tt < TPW; ++tt) wj[tt] = word_j<TPW>(w[tt], j);
-                mma_step<NT, TPW, BF16, false>(wj, xa, L.xlo[j], L.xhi[j], L.lane, j, c);
+                mma_step<NT, TPW, BF16, false, SUB>(wj, xa, L.xlo[j], L.xhi[j], L.lane, j, c);
                 if constexpr (MODE == kModeG32) {
                     if (j & 1) {
                         float2 S32[NT];
                         load_sums<NT>(v.sx32, 2 * a + (j >> 1), v.sstride, L, S32);
-                        fold<NT, TPW, BF16>(v, L, t0, 2 * a + (j >> 1), S32, c, acc);
+                        fold<NT, TPW, BF16, SUB>(v, L, t0, 2 * a + (j >> 1), S32, c, acc);
                         zero_acc<NT, TPW>(c);
                     }
                 }
@@ -552,7 +570,7 @@ W4_DEV void consume(const StageView& v, const Lane& L, int t0, int ab, int ae, i
                     S[nt].y += S64[nt].y;
                 }
                 if ((64 * (v.a0 + a + 1)) % g == 0 || a == ae - 1) {
-                    fold<NT, TPW, BF16>(v, L, t0, (64 * (v.a0 + a)) / g - v.gfirst, S, c, acc);
+                    fold<NT, TPW, BF16, SUB>(v, L, t0, (64 * (v.a0 + a)) / g - v.gfirst, S, c, acc);
                     zero_acc<NT, TPW>(c);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) S[nt] = make_float2(0.0f, 0.0f);
@@ -958,8 +976,51 @@ W4_DEV void combine_sets(unsigned char* xchg, int set, int t0, const Lane& L, fl
     }
 }
 
-template <int NT, int TPW>
-W4_DEV void store_rows(const DecodeParams& p, int band, int t0, const Lane& L, const float (&acc)[TPW][NT][4]) {
+// Y through its epilogue: a thread holds rows r and r + 8 of its tiles, for gated weights
+// an output's gate and up.
+template <int NT, int TPW, bool SUB>
+W4_DEV void store_rows_epi(const DecodeParams& p, const w4e::Epilogue& epi, int band, int t0, const Lane& L,
+                           const float (&acc)[TPW][NT][4]) {
+    const int tb = band_tiles(p, band);
+#pragma unroll
+    for (int tt = 0; tt < TPW; ++tt) {
+        if (t0 + tt >= tb) continue;
+        const int n0 = band * kBandRows + 16 * (t0 + tt) + L.g8, n1 = n0 + 8;
+        const float b0 = epi.bias ? w4e::load_elem(epi.bias, epi.bias_dtype, n0) : 0.0f;
+        const float b1 = epi.bias ? w4e::load_elem(epi.bias, epi.bias_dtype, n1) : 0.0f;
+        const int f = band * (kBandRows / 2) + 8 * (t0 + tt) + L.g8;   // gated output column
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int m = 8 * nt + 2 * L.q + e;
+                if (m >= p.M) continue;
+                float v0 = w4e::activate(epi.act, fmaf(acc[tt][nt][e], SUB ? 16777216.0f : 1.0f, b0));
+                float v1 = fmaf(acc[tt][nt][e + 2], SUB ? 1048576.0f : 1.0f, b1);
+                if (epi.gated) {
+                    v0 *= v1;
+                    if (epi.residual) v0 += w4e::load_elem(epi.residual, epi.res_dtype, (size_t)m * epi.ldr + f);
+                    store_elem(p, (size_t)m * epi.ldy + f, v0);
+                } else {
+                    v1 = w4e::activate(epi.act, v1);
+                    if (epi.residual) {
+                        v0 += w4e::load_elem(epi.residual, epi.res_dtype, (size_t)m * epi.ldr + n0);
+                        v1 += w4e::load_elem(epi.residual, epi.res_dtype, (size_t)m * epi.ldr + n1);
+                    }
+                    store_elem(p, (size_t)m * epi.ldy + n0, v0);
+                    store_elem(p, (size_t)m * epi.ldy + n1, v1);
+                }
+            }
+    }
+}
+
+template <int NT, int TPW, bool EPI, bool SUB>
+W4_DEV void store_rows(const DecodeParams& p, const w4e::Epilogue& epi, int band, int t0, const Lane& L,
+                       const float (&acc)[TPW][NT][4]) {
+    if constexpr (EPI) {
+        store_rows_epi<NT, TPW, SUB>(p, epi, band, t0, L, acc);
+        return;
+    }
     const int tb = band_tiles(p, band);
 #pragma unroll
     for (int tt = 0; tt < TPW; ++tt) {
@@ -977,9 +1038,9 @@ W4_DEV void store_rows(const DecodeParams& p, int band, int t0, const Lane& L, c
 
 // A part that does not complete its band (set-0 threads, after combine_sets): a whole band
 // is stored; a contributor part publishes this CTA's share into its slots.
-template <int NT, int TPW>
-W4_DEV void flush_part(const DecodeParams& p, int band, int pe, int cta, int t0, const Lane& L,
-                       const float (&acc)[TPW][NT][4]) {
+template <int NT, int TPW, bool EPI = false, bool SUB = false>
+W4_DEV void flush_part(const DecodeParams& p, const w4e::Epilogue& epi, int band, int pe, int cta, int t0,
+                       const Lane& L, const float (&acc)[TPW][NT][4]) {
     constexpr int kSlot = kTilesPerBand * NT * 4 * 32;
     const int tb = band_tiles(p, band);
     if (pe < (band + 1) * p.KU) {
@@ -996,14 +1057,14 @@ W4_DEV void flush_part(const DecodeParams& p, int band, int pe, int cta, int t0,
         }
         return;
     }
-    store_rows<NT, TPW>(p, band, t0, L, acc);
+    store_rows<NT, TPW, EPI, SUB>(p, epi, band, t0, L, acc);
 }
 
 // The CTA's last part holds the band's last unit and started inside the band: add the
 // contributors' shares (CTA order) before this CTA's own, then store.  Runs after the part
 // loop, on every MMA warp (named barriers on the shared path).
-template <int NT, int TPW>
-W4_DEV void complete_band(const DecodeParams& p, unsigned char* smem, unsigned char* xchg, volatile int* s_abort,
+template <int NT, int TPW, bool EPI = false, bool SUB = false>
+W4_DEV void complete_band(const DecodeParams& p, const w4e::Epilogue& epi, unsigned char* smem, unsigned char* xchg, volatile int* s_abort,
                           int band, int cta, int set, int t0, const Lane& L, bool aborted,
                           float (&acc)[TPW][NT][4]) {
     using C = Cfg<NT>;
@@ -1030,7 +1091,7 @@ W4_DEV void complete_band(const DecodeParams& p, unsigned char* smem, unsigned c
     }
     named_bar_sync(2, 32 * C::mma_warps);
     if (set > 0 || aborted || *s_abort) return;
-    store_rows<NT, TPW>(p, band, t0, L, acc);
+    store_rows<NT, TPW, EPI, SUB>(p, epi, band, t0, L, acc);
 }
 
 // ---------------------------------------------------------------- the kernel
@@ -1078,12 +1139,12 @@ struct Ring {
     }
 };
 
-template <int NT, bool BF16, int MODE, bool PERM>
-__global__ void __launch_bounds__(Cfg<NT>::threads, 1)
-    decode_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_sc,
-                  const __grid_constant__ CUtensorMap tmap_zr, const DecodeParams p) {
+template <int NT, bool BF16, int MODE, bool PERM, bool EPI>
+W4_DEV void decode_body(const CUtensorMap& tmap_x, const CUtensorMap& tmap_sc, const CUtensorMap& tmap_zr,
+                        const DecodeParams& p, const w4e::Epilogue& epi) {
     using C = Cfg<NT>;
     constexpr bool GIDX = MODE == kModeGidx;
+    constexpr bool SUB = EPI && !BF16 && !GIDX;   // codes as subnormal fp16 (unpack_biased)
     constexpr int UPS = C::aps / 2;   // units per stage
     const int S = p.stages;
     extern __shared__ unsigned char smem_raw[];
@@ -1290,7 +1351,7 @@ __global__ void __launch_bounds__(Cfg<NT>::threads, 1)
                     if constexpr (GIDX) consume_gidx<NT, TPW>(v, p, L, band, t0, ab, ae, st + p.off_gi, acc);
                     else if constexpr (MODE == kModeNvfp4 || MODE == kModeMxfp4)
                         consume_fp4<NT, TPW, MODE>(v, L, t0, ab, ae, p.tscale ? __ldg(p.tscale) : 1.0f, acc);
-                    else consume<NT, TPW, BF16, MODE>(v, L, t0, ab, ae, g, acc);
+                    else consume<NT, TPW, BF16, MODE, SUB>(v, L, t0, ab, ae, g, acc);
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&empty[r.s]);
@@ -1298,13 +1359,29 @@ __global__ void __launch_bounds__(Cfg<NT>::threads, 1)
             combine_sets<NT, TPW>(xchg, set, t0, L, acc);
             // the part that completes its band is the last one: finished after the loop
             if (pe == (band + 1) * p.KU && ps > band * p.KU) continue;
-            if (set == 0 && !aborted) flush_part<NT, TPW>(p, band, pe, cta, t0, L, acc);
+            if (set == 0 && !aborted) flush_part<NT, TPW, EPI, SUB>(p, epi, band, pe, cta, t0, L, acc);
             zero_acc<NT, TPW>(acc);
         }
         if (u0 > it.b0 * p.KU && u1 >= (it.b0 + 1) * p.KU)
-            complete_band<NT, TPW>(p, smem, xchg, s_abort, it.b0, cta, set, t0, L, aborted, acc);
+            complete_band<NT, TPW, EPI, SUB>(p, epi, smem, xchg, s_abort, it.b0, cta, set, t0, L, aborted, acc);
     }
     }
+}
+
+template <int NT, bool BF16, int MODE, bool PERM>
+__global__ void __launch_bounds__(Cfg<NT>::threads, 1)
+    decode_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_sc,
+                  const __grid_constant__ CUtensorMap tmap_zr, const DecodeParams p) {
+    decode_body<NT, BF16, MODE, PERM, false>(tmap_x, tmap_sc, tmap_zr, p, w4e::Epilogue{});
+}
+
+// The same product with an epilogue.  A kernel of its own: the plain product keeps its
+// registers and its bits.
+template <int NT, bool BF16, int MODE, bool PERM>
+__global__ void __launch_bounds__(Cfg<NT>::threads, 1)
+    decode_epi_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_sc,
+                      const __grid_constant__ CUtensorMap tmap_zr, const DecodeParams p, const w4e::Epilogue epi) {
+    decode_body<NT, BF16, MODE, PERM, true>(tmap_x, tmap_sc, tmap_zr, p, epi);
 }
 
 }  // namespace w4d

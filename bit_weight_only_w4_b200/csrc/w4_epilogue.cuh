@@ -1,0 +1,50 @@
+// w4_epilogue.cuh -- epilogue arithmetic of the W4A16 product: bias, activation, gate and
+// residual applied to the fp32 sums before their one rounding to the output type.
+//
+//   t[m,n] = sum_k X'[m,k] What[n,k] + bias[n]
+//   plain:  Y[m,n] = act(t[m,n]) + residual[m,n]
+//   gated:  packed rows alternate in blocks of 8 gate rows and 8 up rows, so output column
+//           f = 8 b + r has its gate in packed row 16 b + r and its up in row 16 b + 8 + r:
+//           Y[m,f] = act(t[m, 16 b + r]) * t[m, 16 b + 8 + r] + residual[m,f]
+// Blocks of 8 rows, because both matrix paths hold rows r and r + 8 of a 16-row tile in
+// one place: the two row halves of a warp MMA's accumulator are registers of one thread
+// (decode), and 16 consecutive staged rows are one thread's 16-byte output piece
+// (prefill).  Halves [gate; up] would put the two values into different CTAs.
+#pragma once
+#include "w4_common.cuh"
+
+namespace w4e {
+
+enum : int { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4 };
+
+struct Epilogue {
+    const void* bias;       // [N] in packed row order, or null
+    const void* residual;   // [M, N_out], rows ldr apart, or null
+    long long ldr, ldy;     // elements between rows of the residual and of Y
+    int bias_dtype, res_dtype;
+    int act, gated;
+};
+
+// Plain loads, not the read-only path: the residual may be Y itself, or the output of a
+// kernel that this one overlaps up to griddepcontrol.wait.
+W4_DEV float load_elem(const void* p, int dtype, size_t i) {
+    if (dtype == 2) return reinterpret_cast<const float*>(p)[i];
+    if (dtype == 1) return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p)[i]);
+    return __half2float(reinterpret_cast<const __half*>(p)[i]);
+}
+
+// One fp32 activation.  The exponential is the hardware's 2^x (a few ulp of fp32 over the
+// range where the result is not negligible): far below the rounding to a 16-bit Y.
+//   silu      x / (1 + e^-x)
+//   gelu      x Phi(x) = x/2 erfc(-x / sqrt 2)        (erfc keeps the negative tail's digits)
+//   gelu_tanh x/2 (1 + tanh u) = x / (1 + e^-2u),  u = sqrt(2/pi) (x + 0.044715 x^3)
+W4_DEV float activate(int act, float x) {
+    if (act == kActNone) return x;
+    if (act == kActRelu) return x < 0.0f ? 0.0f : x;   // NaN stays NaN
+    if (act == kActGelu) return 0.5f * x * erfcf(-0.70710678118654752f * x);
+    const float u = act == kActSilu ? x : 1.5957691216057308f * fmaf(0.044715f * x * x, x, x);
+    // for e^-u beyond 2^126 the quotient is below 2^-100: __fdividef's zero there is right
+    return __fdividef(x, 1.0f + __expf(-u));
+}
+
+}  // namespace w4e

@@ -31,6 +31,7 @@
 // accumulates in one tensor-memory buffer.
 #pragma once
 #include "w4_common.cuh"
+#include "w4_epilogue.cuh"
 #include "w4_fp4.cuh"
 
 namespace w4p {
@@ -216,9 +217,51 @@ W4_DEV bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_fl
     return false;
 }
 
-template <bool BF16, int WM>
-__global__ void __launch_bounds__(kThreads, 1)
-    prefill_kernel(const __grid_constant__ CUtensorMap tmap_x, const PrefillParams p) {
+// The epilogue's copy-out: 16 consecutive staged fp32 rows (packed rows 16 b ..) of one
+// token become 8 outputs (gated: 8 gate rows, 8 up rows) or 8 of the 16 (half: which 8).
+// Loads and stores are 16-byte pieces: rows of Y and of the residual start on 16-byte
+// boundaries (checked on the host).
+W4_DEV void add_residual8(const w4e::Epilogue& epi, size_t idx, float (&v)[8]) {
+    if (epi.res_dtype == 2) {
+        const float4* r = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(epi.residual) + idx);
+        const float4 a = r[0], b = r[1];
+        v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+        v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+        return;
+    }
+    const uint4 r = *reinterpret_cast<const uint4*>(reinterpret_cast<const __half*>(epi.residual) + idx);
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = epi.res_dtype == 1 ? unpack2<true>(w[i]) : unpack2<false>(w[i]);
+        v[2 * i] += f.x;
+        v[2 * i + 1] += f.y;
+    }
+}
+
+W4_DEV void store8(void* Y, int dtype, size_t idx, const float (&v)[8]) {
+    if (dtype == 2) {
+        float4* o = reinterpret_cast<float4*>(reinterpret_cast<float*>(Y) + idx);
+        o[0] = make_float4(v[0], v[1], v[2], v[3]);
+        o[1] = make_float4(v[4], v[5], v[6], v[7]);
+        return;
+    }
+    uint4 o;
+    if (dtype == 1)
+        o = make_uint4(pack2<true>(v[0], v[1]), pack2<true>(v[2], v[3]), pack2<true>(v[4], v[5]), pack2<true>(v[6], v[7]));
+    else
+        o = make_uint4(pack2<false>(v[0], v[1]), pack2<false>(v[2], v[3]), pack2<false>(v[4], v[5]), pack2<false>(v[6], v[7]));
+    *reinterpret_cast<uint4*>(reinterpret_cast<__half*>(Y) + idx) = o;
+}
+
+W4_DEV void load_staged8(const float* src, float (&v)[8]) {
+    const float4 a = reinterpret_cast<const float4*>(src)[0], b = reinterpret_cast<const float4*>(src)[1];
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+
+template <bool BF16, int WM, bool EPI>
+W4_DEV void prefill_body(const CUtensorMap& tmap_x, const PrefillParams& p, const w4e::Epilogue& epi) {
     constexpr bool GIDX = WM == kWGidx;
     constexpr bool FP4 = WM == kWNvfp4 || WM == kWMxfp4;
     constexpr bool ONEBUF = GIDX || FP4;   // scale in the weights: one partial over the whole K
@@ -536,6 +579,46 @@ __global__ void __launch_bounds__(kThreads, 1)
             // along N.  The next tile's MMAs proceed meanwhile.
             const int cpr = BN * esz / 16;               // 16-byte pieces per token row
             const int ncols = min(BN, p.N - n0);         // a multiple of 16 (N % 16 == 0)
+            if constexpr (EPI) {
+                // the same staging in fp32, bias added on the way in (one row a thread);
+                // activation, gate and residual on the way out, 8 outputs a thread
+                const float bias = (epi.bias && row_ok) ? w4e::load_elem(epi.bias, epi.bias_dtype, n) : 0.0f;
+                float* ys = reinterpret_cast<float*>(yt);
+                const int pieces = epi.gated ? BN / 16 : BN / 8;
+                const int npc = min(BN, p.N - n0) / (epi.gated ? 16 : 8);
+                const int c0 = epi.gated ? n0 / 2 : n0;
+#pragma unroll
+                for (int ck = 0; ck < BM / 2 / kYChunk; ++ck) {
+                    if (ok) {
+#pragma unroll
+                        for (int i = 0; i < kYChunk; ++i) ys[(h * kYChunk + i) * BN + row] = acc[ck * kYChunk + i] + bias;
+                    }
+                    named_bar_sync(1, 256);
+                    if (ok) {
+#pragma unroll 1
+                        for (int cc = 32 * e + lane; cc < 2 * kYChunk * pieces; cc += 256) {
+                            const int m = cc / pieces, pc = cc - m * pieces;
+                            const int mm = m0 + (m / kYChunk) * (BM / 2) + ck * kYChunk + m % kYChunk;
+                            if (mm >= p.M || pc >= npc) continue;
+                            float v[8];
+                            if (epi.gated) {
+                                float up[8];
+                                load_staged8(ys + m * BN + 16 * pc, v);
+                                load_staged8(ys + m * BN + 16 * pc + 8, up);
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) v[i] = w4e::activate(epi.act, v[i]) * up[i];
+                            } else {
+                                load_staged8(ys + m * BN + 8 * pc, v);
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) v[i] = w4e::activate(epi.act, v[i]);
+                            }
+                            if (epi.residual) add_residual8(epi, (size_t)mm * epi.ldr + c0 + 8 * pc, v);
+                            store8(p.Y, p.out_dtype, (size_t)mm * epi.ldy + c0 + 8 * pc, v);
+                        }
+                    }
+                    named_bar_sync(1, 256);   // the buffer is free for the next block
+                }
+            } else {
 #pragma unroll
             for (int ck = 0; ck < BM / 2 / kYChunk; ++ck) {
                 if (ok) {
@@ -561,6 +644,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 named_bar_sync(1, 256);   // the buffer is free for the next block
             }
+            }
         }
     }
 
@@ -570,6 +654,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         tmem_dealloc(tmem_base, kTmemCols);
     }
+}
+
+template <bool BF16, int WM>
+__global__ void __launch_bounds__(kThreads, 1)
+    prefill_kernel(const __grid_constant__ CUtensorMap tmap_x, const PrefillParams p) {
+    prefill_body<BF16, WM, false>(tmap_x, p, w4e::Epilogue{});
+}
+
+// The same product with an epilogue (a kernel of its own: the plain product keeps its code).
+template <bool BF16, int WM>
+__global__ void __launch_bounds__(kThreads, 1)
+    prefill_epi_kernel(const __grid_constant__ CUtensorMap tmap_x, const PrefillParams p, const w4e::Epilogue epi) {
+    prefill_body<BF16, WM, true>(tmap_x, p, epi);
 }
 
 // X'[m,k] = X[m,k] * s_inv[k], rounded to the activation type (for the prefill path,

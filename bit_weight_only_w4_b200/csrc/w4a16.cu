@@ -3,6 +3,7 @@
 // w4_quant.cuh, w4_decode.cuh and w4_prefill.cuh; nothing here touches tensor data.
 #include <algorithm>
 #include <climits>
+#include <cmath>
 #include <cstring>
 #include <mutex>
 
@@ -14,6 +15,8 @@
 #include "w4_actorder.cuh"
 #include "w4_chain.cuh"
 #include "w4_awq.cuh"
+#include "w4_rope.cuh"
+#include "w4_attention.cuh"
 
 namespace {
 
@@ -41,6 +44,9 @@ w4_status check_layer_shape(int64_t N, int64_t K, int32_t group_size) {
     if (group_size != 32 && group_size % 64 != 0) return W4_ERR_UNSUPPORTED;
     return W4_OK;
 }
+
+bool valid_dtype(w4_dtype t) { return t == W4_F16 || t == W4_BF16 || t == W4_F32; }
+int dtype_bytes(w4_dtype t) { return t == W4_F32 ? 4 : 2; }
 
 int current_device() {
     int dev = 0;
@@ -196,12 +202,16 @@ bool decode_x_resident(int64_t M, int64_t K) {
     return up(M * K * 2, 128) + up((K / 32 + K / 64 + K / 128) * sstride * 4, 128) <= 80 * 1024;
 }
 
-template <int NT, bool BF16, int MODE, bool PERM>
-w4_status launch_decode(w4d::DecodeParams p, const void* X, unsigned char* ws, size_t pre_off, int dev,
-                        cudaStream_t stream) {
+// epi: null for the plain product.
+template <int NT, bool BF16, int MODE, bool PERM, bool EPI>
+w4_status launch_decode_kernel(w4d::DecodeParams p, const void* X, unsigned char* ws, size_t pre_off, int dev,
+                               const w4e::Epilogue* epi, cudaStream_t stream) {
     using C = w4d::Cfg<NT>;
     constexpr bool GIDX = MODE == w4d::kModeGidx;
-    auto kernel = w4d::decode_kernel<NT, BF16, MODE, PERM>;
+    const auto kernel = [] {
+        if constexpr (EPI) return w4d::decode_epi_kernel<NT, BF16, MODE, PERM>;
+        else return w4d::decode_kernel<NT, BF16, MODE, PERM>;
+    }();
     static std::once_flag flags[kMaxDevices];
     constexpr int kMaxSmem = 227 * 1024;
     bool attr_ok = true;
@@ -302,8 +312,20 @@ w4_status launch_decode(w4d::DecodeParams p, const void* X, unsigned char* ws, s
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kernel, map_x, map_sc, map_zr, p) != cudaSuccess) return W4_ERR_CUDA;
+    cudaError_t launched;
+    if constexpr (EPI) launched = cudaLaunchKernelEx(&cfg, kernel, map_x, map_sc, map_zr, p, *epi);
+    else launched = cudaLaunchKernelEx(&cfg, kernel, map_x, map_sc, map_zr, p);
+    if (launched != cudaSuccess) return W4_ERR_CUDA;
     return launch_status();
+}
+
+template <int NT, bool BF16, int MODE, bool PERM>
+w4_status launch_decode(const w4d::DecodeParams& p, const void* X, unsigned char* ws, size_t pre_off, int dev,
+                        const w4e::Epilogue* epi, cudaStream_t stream) {
+    if constexpr (MODE != w4d::kModeNvfp4 && MODE != w4d::kModeMxfp4) {
+        if (epi) return launch_decode_kernel<NT, BF16, MODE, PERM, true>(p, X, ws, pre_off, dev, epi, stream);
+    }
+    return launch_decode_kernel<NT, BF16, MODE, PERM, false>(p, X, ws, pre_off, dev, nullptr, stream);
 }
 
 // Group handling: one fold per 128-channel half stage when groups are whole multiples of
@@ -318,39 +340,42 @@ int decode_mode(int64_t K, int32_t g, bool gidx) {
 
 template <int NT, bool BF16, bool PERM>
 w4_status dispatch_mode(int mode, w4d::DecodeParams p, const void* X, unsigned char* ws, size_t pre_off, int dev,
-                        cudaStream_t s) {
+                        const w4e::Epilogue* epi, cudaStream_t s) {
     if constexpr (!BF16 && !PERM) {
-        if (mode == w4d::kModeGidx) return launch_decode<NT, false, w4d::kModeGidx, false>(p, X, ws, pre_off, dev, s);
-        if (mode == w4d::kModeNvfp4) return launch_decode<NT, false, w4d::kModeNvfp4, false>(p, X, ws, pre_off, dev, s);
-        if (mode == w4d::kModeMxfp4) return launch_decode<NT, false, w4d::kModeMxfp4, false>(p, X, ws, pre_off, dev, s);
+        if (mode == w4d::kModeGidx) return launch_decode<NT, false, w4d::kModeGidx, false>(p, X, ws, pre_off, dev, epi, s);
+        if (mode == w4d::kModeNvfp4) return launch_decode<NT, false, w4d::kModeNvfp4, false>(p, X, ws, pre_off, dev, epi, s);
+        if (mode == w4d::kModeMxfp4) return launch_decode<NT, false, w4d::kModeMxfp4, false>(p, X, ws, pre_off, dev, epi, s);
     } else {
         if (mode == w4d::kModeGidx || mode == w4d::kModeNvfp4 || mode == w4d::kModeMxfp4) return W4_ERR_UNSUPPORTED;
     }
-    if (mode == w4d::kModeHalf) return launch_decode<NT, BF16, w4d::kModeHalf, PERM>(p, X, ws, pre_off, dev, s);
-    if (mode == w4d::kModeG32) return launch_decode<NT, BF16, w4d::kModeG32, PERM>(p, X, ws, pre_off, dev, s);
-    return launch_decode<NT, BF16, w4d::kModeAtom, PERM>(p, X, ws, pre_off, dev, s);
+    if (mode == w4d::kModeHalf) return launch_decode<NT, BF16, w4d::kModeHalf, PERM>(p, X, ws, pre_off, dev, epi, s);
+    if (mode == w4d::kModeG32) return launch_decode<NT, BF16, w4d::kModeG32, PERM>(p, X, ws, pre_off, dev, epi, s);
+    return launch_decode<NT, BF16, w4d::kModeAtom, PERM>(p, X, ws, pre_off, dev, epi, s);
 }
 
 template <bool BF16>
 w4_status dispatch_decode(int mode, w4d::DecodeParams p, const void* X, unsigned char* ws, size_t pre_off, int dev,
-                          cudaStream_t s) {
+                          const w4e::Epilogue* epi, cudaStream_t s) {
     // act-order columns gathered while the resident X' is prepared: one token tile only
-    if (p.perm) return decode_tiles_for(p.M) == 1 ? dispatch_mode<1, BF16, true>(mode, p, X, ws, pre_off, dev, s)
+    if (p.perm) return decode_tiles_for(p.M) == 1 ? dispatch_mode<1, BF16, true>(mode, p, X, ws, pre_off, dev, epi, s)
                                                   : W4_ERR_UNSUPPORTED;
     switch (decode_tiles_for(p.M)) {
-        case 1: return dispatch_mode<1, BF16, false>(mode, p, X, ws, pre_off, dev, s);
-        case 2: return dispatch_mode<2, BF16, false>(mode, p, X, ws, pre_off, dev, s);
-        case 4: return dispatch_mode<4, BF16, false>(mode, p, X, ws, pre_off, dev, s);
-        default: return dispatch_mode<8, BF16, false>(mode, p, X, ws, pre_off, dev, s);
+        case 1: return dispatch_mode<1, BF16, false>(mode, p, X, ws, pre_off, dev, epi, s);
+        case 2: return dispatch_mode<2, BF16, false>(mode, p, X, ws, pre_off, dev, epi, s);
+        case 4: return dispatch_mode<4, BF16, false>(mode, p, X, ws, pre_off, dev, epi, s);
+        default: return dispatch_mode<8, BF16, false>(mode, p, X, ws, pre_off, dev, epi, s);
     }
 }
 
 // ---------------------------------------------------------------- prefill launch plan
-template <bool BF16, int WM>
-w4_status launch_prefill(const CUtensorMap& map, const w4p::PrefillParams& p, int dev,
-                         cudaStream_t stream) {
+template <bool BF16, int WM, bool EPI>
+w4_status launch_prefill_kernel(const CUtensorMap& map, const w4p::PrefillParams& p, int dev,
+                                const w4e::Epilogue* epi, cudaStream_t stream) {
     static std::once_flag flags[kMaxDevices];
-    auto k = w4p::prefill_kernel<BF16, WM>;
+    const auto k = [] {
+        if constexpr (EPI) return w4p::prefill_epi_kernel<BF16, WM>;
+        else return w4p::prefill_kernel<BF16, WM>;
+    }();
     if (!ensure_smem(k, w4p::SmemLayout::bytes, flags, dev)) return W4_ERR_CUDA;
     // the kernel's per-warpgroup register split assumes this many registers a thread at
     // launch; any other build would make its register increase wait forever
@@ -376,8 +401,21 @@ w4_status launch_prefill(const CUtensorMap& map, const w4p::PrefillParams& p, in
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, k, map, p) != cudaSuccess) return W4_ERR_CUDA;
+    cudaError_t launched;
+    if constexpr (EPI) launched = cudaLaunchKernelEx(&cfg, k, map, p, *epi);
+    else launched = cudaLaunchKernelEx(&cfg, k, map, p);
+    if (launched != cudaSuccess) return W4_ERR_CUDA;
     return launch_status();
+}
+
+// epi: null for the plain product.
+template <bool BF16, int WM>
+w4_status launch_prefill(const CUtensorMap& map, const w4p::PrefillParams& p, int dev, cudaStream_t stream,
+                         const w4e::Epilogue* epi = nullptr) {
+    if constexpr (WM == w4p::kWInt4 || WM == w4p::kWGidx) {
+        if (epi) return launch_prefill_kernel<BF16, WM, true>(map, p, dev, epi, stream);
+    }
+    return launch_prefill_kernel<BF16, WM, false>(map, p, dev, nullptr, stream);
 }
 
 }  // namespace
@@ -520,7 +558,7 @@ static w4_status gemm_impl(const void* X, w4_dtype act_dtype, int64_t M, int64_t
                            const uint32_t* qweight, const void* scales, const void* zeros,
                            const int32_t* g_idx, const int32_t* perm, int32_t group_size,
                            const float* s_inv, void* Y, w4_dtype out_dtype, void* workspace,
-                           size_t workspace_bytes, w4_stream_t stream);
+                           size_t workspace_bytes, w4_stream_t stream, const w4e::Epilogue* epi = nullptr);
 
 w4_status w4a16_gemm(const void* X, w4_dtype act_dtype, int64_t M, int64_t N, int64_t K,
                      const uint32_t* qweight, const void* scales, const void* zeros,
@@ -535,7 +573,7 @@ static w4_status gemm_impl(const void* X, w4_dtype act_dtype, int64_t M, int64_t
                            const uint32_t* qweight, const void* scales, const void* zeros,
                            const int32_t* g_idx, const int32_t* perm, int32_t group_size,
                            const float* s_inv, void* Y, w4_dtype out_dtype, void* workspace,
-                           size_t workspace_bytes, w4_stream_t stream) {
+                           size_t workspace_bytes, w4_stream_t stream, const w4e::Epilogue* epi) {
     if (M < 0) return W4_ERR_INVALID_ARG;
     if (act_dtype != W4_F16 && act_dtype != W4_BF16) return W4_ERR_INVALID_ARG;
     if (out_dtype != W4_F16 && out_dtype != W4_BF16 && out_dtype != W4_F32) return W4_ERR_INVALID_ARG;
@@ -581,8 +619,8 @@ static w4_status gemm_impl(const void* X, w4_dtype act_dtype, int64_t M, int64_t
         unsigned char* ws = reinterpret_cast<unsigned char*>(workspace);
         const int mode = decode_mode(K, group_size, gidx);
         const size_t pre_off = pre_offset(8, sm_count(dev));
-        if (bf16) return dispatch_decode<true>(mode, p, X, ws, pre_off, dev, strm);
-        return dispatch_decode<false>(mode, p, X, ws, pre_off, dev, strm);
+        if (bf16) return dispatch_decode<true>(mode, p, X, ws, pre_off, dev, epi, strm);
+        return dispatch_decode<false>(mode, p, X, ws, pre_off, dev, epi, strm);
     }
 
     const void* Xeff = X;
@@ -612,9 +650,9 @@ static w4_status gemm_impl(const void* X, w4_dtype act_dtype, int64_t M, int64_t
     p.out_dtype = (int)out_dtype;
     p.KA = (int)(K / 64);
     p.tiles = (int)(N / 16);
-    if (bf16) return launch_prefill<true, w4p::kWInt4>(map, p, dev, strm);
-    return gidx ? launch_prefill<false, w4p::kWGidx>(map, p, dev, strm)
-                : launch_prefill<false, w4p::kWInt4>(map, p, dev, strm);
+    if (bf16) return launch_prefill<true, w4p::kWInt4>(map, p, dev, strm, epi);
+    return gidx ? launch_prefill<false, w4p::kWGidx>(map, p, dev, strm, epi)
+                : launch_prefill<false, w4p::kWInt4>(map, p, dev, strm, epi);
 }
 
 size_t w4a16_workspace_bytes_perm(int64_t M, int64_t N, int64_t K, int32_t group_size) {
@@ -627,11 +665,11 @@ size_t w4a16_workspace_bytes_perm(int64_t M, int64_t N, int64_t K, int32_t group
     return perm_gather_offset(M, K, sms) + (size_t)(((size_t)M * (size_t)K * 2 + 255) / 256 * 256);
 }
 
-w4_status w4a16_gemm_perm(const void* X, w4_dtype act_dtype, int64_t M, int64_t N, int64_t K,
+static w4_status gemm_perm_impl(const void* X, w4_dtype act_dtype, int64_t M, int64_t N, int64_t K,
                           const uint32_t* qweight, const void* scales, const void* zeros,
                           const int32_t* perm, int32_t group_size, const float* s_inv, void* Y,
                           w4_dtype out_dtype, void* workspace, size_t workspace_bytes,
-                          w4_stream_t stream) {
+                          w4_stream_t stream, const w4e::Epilogue* epi = nullptr) {
     if (M < 0) return W4_ERR_INVALID_ARG;
     if (act_dtype != W4_F16 && act_dtype != W4_BF16) return W4_ERR_INVALID_ARG;
     w4_status st = check_layer_shape(N, K, group_size);
@@ -648,7 +686,7 @@ w4_status w4a16_gemm_perm(const void* X, w4_dtype act_dtype, int64_t M, int64_t 
     if (dev < 0 || dev >= kMaxDevices) return W4_ERR_CUDA;
     if (M <= kDecodeMaxM && decode_x_resident(M, K))   // the decode kernel gathers while preparing X'
         return gemm_impl(X, act_dtype, M, N, K, qweight, scales, zeros, nullptr, perm, group_size, s_inv, Y,
-                         out_dtype, workspace, workspace_bytes, stream);
+                         out_dtype, workspace, workspace_bytes, stream, epi);
     cudaStream_t strm = as_stream(stream);
     void* xp = reinterpret_cast<unsigned char*>(workspace) + perm_gather_offset(M, K, sm_count(dev));
     const size_t chunks = (size_t)M * (size_t)K / 8;
@@ -658,7 +696,54 @@ w4_status w4a16_gemm_perm(const void* X, w4_dtype act_dtype, int64_t M, int64_t 
     if (cudaGetLastError() != cudaSuccess) return W4_ERR_CUDA;
     // the contiguous-group GEMM on the gathered, already scaled activations
     return gemm_impl(xp, act_dtype, M, N, K, qweight, scales, zeros, nullptr, nullptr, group_size, nullptr, Y,
-                     out_dtype, workspace, workspace_bytes, stream);
+                     out_dtype, workspace, workspace_bytes, stream, epi);
+}
+
+w4_status w4a16_gemm_perm(const void* X, w4_dtype act_dtype, int64_t M, int64_t N, int64_t K,
+                          const uint32_t* qweight, const void* scales, const void* zeros,
+                          const int32_t* perm, int32_t group_size, const float* s_inv, void* Y,
+                          w4_dtype out_dtype, void* workspace, size_t workspace_bytes,
+                          w4_stream_t stream) {
+    return gemm_perm_impl(X, act_dtype, M, N, K, qweight, scales, zeros, perm, group_size, s_inv, Y, out_dtype,
+                          workspace, workspace_bytes, stream);
+}
+
+w4_status w4a16_gemm_epi(const void* X, w4_dtype act_dtype, int64_t M, int64_t N, int64_t K,
+                         const uint32_t* qweight, const void* scales, const void* zeros,
+                         const int32_t* g_idx, const int32_t* perm, int32_t group_size,
+                         const float* s_inv, const w4_epilogue* epi, void* Y, w4_dtype out_dtype,
+                         void* workspace, size_t workspace_bytes, w4_stream_t stream) {
+    if (!epi || (g_idx && perm)) return W4_ERR_INVALID_ARG;
+    if (!valid_dtype(out_dtype) || (epi->bias && !valid_dtype(epi->bias_dtype)) ||
+        (epi->residual && !valid_dtype(epi->residual_dtype)))
+        return W4_ERR_INVALID_ARG;
+    if ((int)epi->activation < W4_ACT_NONE || (int)epi->activation > W4_ACT_GELU_TANH) return W4_ERR_INVALID_ARG;
+    if (epi->gated != 0 && epi->gated != 1) return W4_ERR_INVALID_ARG;
+    w4_status st = check_layer_shape(N, K, group_size);
+    if (st != W4_OK) return st;
+    const int64_t n_out = epi->gated ? N / 2 : N;
+    const int64_t ldy = epi->ldy ? epi->ldy : n_out, ldr = epi->ldr ? epi->ldr : n_out;
+    if (ldy < n_out || (ldy * dtype_bytes(out_dtype)) % 16 != 0) return W4_ERR_INVALID_ARG;
+    if (epi->bias && !aligned(epi->bias, dtype_bytes(epi->bias_dtype))) return W4_ERR_INVALID_ARG;
+    if (epi->residual) {
+        if (ldr < n_out || (ldr * dtype_bytes(epi->residual_dtype)) % 16 != 0 || !aligned(epi->residual, 16))
+            return W4_ERR_INVALID_ARG;
+        if (epi->residual == Y && (ldr != ldy || epi->residual_dtype != out_dtype)) return W4_ERR_INVALID_ARG;
+    }
+    w4e::Epilogue e;
+    e.bias = epi->bias;
+    e.residual = epi->residual;
+    e.ldr = ldr;
+    e.ldy = ldy;
+    e.bias_dtype = (int)epi->bias_dtype;
+    e.res_dtype = (int)epi->residual_dtype;
+    e.act = (int)epi->activation;
+    e.gated = epi->gated;
+    if (perm)
+        return gemm_perm_impl(X, act_dtype, M, N, K, qweight, scales, zeros, perm, group_size, s_inv, Y, out_dtype,
+                              workspace, workspace_bytes, stream, &e);
+    return gemm_impl(X, act_dtype, M, N, K, qweight, scales, zeros, g_idx, nullptr, group_size, s_inv, Y, out_dtype,
+                     workspace, workspace_bytes, stream, &e);
 }
 
 size_t w4_awq_search_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t group_size,
@@ -933,8 +1018,8 @@ extern "C" w4_status w4a16_gemm_noalloc(const void* X, w4_dtype act_dtype, int64
     cudaStream_t strm = as_stream(stream);
     const int mode = decode_mode(K, group_size, gidx);
     const size_t pre_off = pre_offset(kNoAllocMaxTiles, sms);
-    if (bf16) return dispatch_decode<true>(mode, p, X, ws, pre_off, dev, strm);
-    return dispatch_decode<false>(mode, p, X, ws, pre_off, dev, strm);
+    if (bf16) return dispatch_decode<true>(mode, p, X, ws, pre_off, dev, nullptr, strm);
+    return dispatch_decode<false>(mode, p, X, ws, pre_off, dev, nullptr, strm);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -1254,5 +1339,265 @@ extern "C" w4_status w4a16_fp4_gemm(const void* X, w4_dtype act_dtype, int64_t M
     p.tiles = (int)(N / 16);
     const int mode = format == W4_FP4_NVFP4 ? w4d::kModeNvfp4 : w4d::kModeMxfp4;
     return dispatch_decode<false>(mode, p, X, reinterpret_cast<unsigned char*>(workspace),
-                                  pre_offset(8, sm_count(dev)), dev, strm);
+                                  pre_offset(8, sm_count(dev)), dev, nullptr, strm);
+}
+
+// ---------------------------------------------------------------------------------------
+// Rotary positions
+// ---------------------------------------------------------------------------------------
+namespace {
+
+template <int DT, int E>
+w4_status launch_rope(w4r::RopeParams p, int sms, cudaStream_t stream) {
+    const int half = p.rot / 2;
+    // an item is E pairs, two pieces; the tail behind rot is copied two pieces an item
+    p.per_head = half / E + (p.copy_tail ? (p.dim - p.rot + 2 * E - 1) / (2 * E) : 0);
+    // whole tokens fill a block; with few tokens the heads are split so that every SM works
+    const long long per_tok = (long long)p.heads * p.per_head;
+    p.tokens_per_block = (int)std::max<long long>(1, std::min<long long>(w4r::kMaxTokens, 256 / std::max<long long>(1, per_tok)));
+    p.heads_per_block = p.heads;
+    const long long blocks = (p.tokens + p.tokens_per_block - 1) / p.tokens_per_block;
+    if (blocks < sms) {
+        // at least one warp's items a block
+        const int least = std::max(1, (32 + p.per_head - 1) / p.per_head);
+        const int want = (int)((p.heads * blocks + sms - 1) / sms);
+        p.heads_per_block = std::min(p.heads, std::max(least, want));
+    }
+    p.heads_per_block = std::min(p.heads_per_block, 65535);
+    const long long items = (long long)p.tokens_per_block * p.heads_per_block * p.per_head;
+    const int threads = (int)std::min<long long>(w4r::kMaxThreads, std::max<long long>(64, (items + 31) / 32 * 32));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks, (unsigned)((p.heads + p.heads_per_block - 1) / p.heads_per_block));
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)p.tokens_per_block * half * sizeof(float2);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, w4r::rope_kernel<DT, E>, p) != cudaSuccess) return W4_ERR_CUDA;
+    return launch_status();
+}
+
+}  // namespace
+
+extern "C" w4_status w4_rope(const void* X, w4_dtype dtype, int64_t tokens, int32_t heads, int32_t head_dim,
+                             int64_t x_token_stride, int64_t x_head_stride, const int32_t* positions,
+                             const double* inv_freq, int32_t rot_dim, float mscale, int32_t interleaved,
+                             void* Y, int64_t y_token_stride, int64_t y_head_stride, w4_stream_t stream) {
+    if (!valid_dtype(dtype) || tokens < 0 || heads < 0 || head_dim <= 0) return W4_ERR_INVALID_ARG;
+    if (rot_dim < 2 || rot_dim % 2 != 0 || rot_dim > head_dim) return W4_ERR_INVALID_ARG;
+    if ((interleaved != 0 && interleaved != 1) || !std::isfinite(mscale)) return W4_ERR_INVALID_ARG;
+    if (rot_dim / 2 > w4r::kMaxPairs || tokens > INT_MAX / 2 || heads > 65535 || head_dim > 65536) return W4_ERR_UNSUPPORTED;
+    if (tokens == 0 || heads == 0) return W4_OK;
+    const int esz = dtype_bytes(dtype);
+    if (!X || !Y || !positions || !inv_freq) return W4_ERR_INVALID_ARG;
+    if (!aligned(X, esz) || !aligned(Y, esz) || !aligned(positions, 4) || !aligned(inv_freq, 8)) return W4_ERR_INVALID_ARG;
+    if (x_token_stride < 0 || x_head_stride < 0 || y_token_stride < 0 || y_head_stride < 0) return W4_ERR_INVALID_ARG;
+    // outputs that share an element would race
+    if ((tokens > 1 && y_token_stride < head_dim) || (heads > 1 && y_head_stride < head_dim)) return W4_ERR_INVALID_ARG;
+    const bool in_place = X == Y;
+    if (in_place && ((tokens > 1 && x_token_stride != y_token_stride) || (heads > 1 && x_head_stride != y_head_stride)))
+        return W4_ERR_INVALID_ARG;
+    const int dev = current_device();
+    const int sms = dev >= 0 ? sm_count(dev) : 0;
+    if (sms <= 0) return W4_ERR_CUDA;
+    w4r::RopeParams p;
+    p.X = X;
+    p.Y = Y;
+    p.positions = positions;
+    p.inv_freq = inv_freq;
+    p.ldx = x_token_stride;
+    p.hsx = x_head_stride;
+    p.ldy = y_token_stride;
+    p.hsy = y_head_stride;
+    p.tokens = (int)tokens;
+    p.heads = heads;
+    p.dim = head_dim;
+    p.rot = rot_dim;
+    p.interleaved = interleaved;
+    p.copy_tail = (in_place || rot_dim == head_dim) ? 0 : 1;
+    p.mscale = mscale;
+    cudaStream_t strm = as_stream(stream);
+    // 16-byte pieces where every piece starts on a 16-byte boundary
+    const int E = 16 / esz;
+    auto whole = [&](int64_t n, int64_t stride) { return n <= 1 || stride % E == 0; };
+    const bool wide = aligned(X, 16) && aligned(Y, 16) && whole(tokens, x_token_stride) && whole(heads, x_head_stride) &&
+                      whole(tokens, y_token_stride) && whole(heads, y_head_stride) && head_dim % E == 0 &&
+                      (rot_dim / 2) % E == 0;
+    if (dtype == W4_F32) return wide ? launch_rope<2, 4>(p, sms, strm) : launch_rope<2, 1>(p, sms, strm);
+    if (dtype == W4_BF16) return wide ? launch_rope<1, 8>(p, sms, strm) : launch_rope<1, 1>(p, sms, strm);
+    return wide ? launch_rope<0, 8>(p, sms, strm) : launch_rope<0, 1>(p, sms, strm);
+}
+
+extern "C" w4_status w4_rope_freqs(int32_t rot_dim, double theta, w4_rope_scaling scaling, double factor,
+                                   double context, double lo, double hi, double* inv_freq, float* mscale) {
+    if (!inv_freq || !mscale) return W4_ERR_INVALID_ARG;
+    if (rot_dim < 2 || rot_dim % 2 != 0 || rot_dim / 2 > w4r::kMaxPairs) return W4_ERR_INVALID_ARG;
+    if (!(theta > 1.0) || !std::isfinite(theta)) return W4_ERR_INVALID_ARG;
+    if ((int)scaling < W4_ROPE_PLAIN || (int)scaling > W4_ROPE_RAMP) return W4_ERR_INVALID_ARG;
+    if (scaling != W4_ROPE_PLAIN && (!(factor > 0.0) || !std::isfinite(factor))) return W4_ERR_INVALID_ARG;
+    if (scaling == W4_ROPE_BASE && rot_dim <= 2) return W4_ERR_INVALID_ARG;
+    const bool banded = scaling == W4_ROPE_BANDS || scaling == W4_ROPE_RAMP;
+    if (banded && (!(context > 0.0) || !std::isfinite(context) || !(lo > 0.0) || !(hi > lo) || !std::isfinite(hi)))
+        return W4_ERR_INVALID_ARG;
+    const double two_pi = 6.283185307179586477;
+    const double base = scaling == W4_ROPE_BASE ? theta * std::pow(factor, (double)rot_dim / (rot_dim - 2)) : theta;
+    // the (fractional) pair index that turns r times within the context
+    auto pair_of = [&](double r) { return rot_dim * std::log(context / (r * two_pi)) / (2.0 * std::log(theta)); };
+    double first = 0.0, last = 0.0;
+    if (scaling == W4_ROPE_RAMP) {
+        first = std::max(std::floor(pair_of(hi)), 0.0);
+        last = std::min(std::ceil(pair_of(lo)), (double)(rot_dim - 1));
+        if (last <= first) last = first + 0.001;
+    }
+    for (int i = 0; i < rot_dim / 2; ++i) {
+        const double f = std::pow(base, -2.0 * i / rot_dim);
+        double keep = 1.0;   // share of the unchanged frequency
+        if (scaling == W4_ROPE_LINEAR) keep = 0.0;
+        else if (scaling == W4_ROPE_BANDS) keep = std::min(1.0, std::max(0.0, (context * f / two_pi - lo) / (hi - lo)));
+        else if (scaling == W4_ROPE_RAMP) keep = 1.0 - std::min(1.0, std::max(0.0, (i - first) / (last - first)));
+        inv_freq[i] = keep == 1.0 ? f : keep * f + (1.0 - keep) * f / factor;
+    }
+    *mscale = (scaling == W4_ROPE_RAMP && factor > 1.0) ? (float)(0.1 * std::log(factor) + 1.0) : 1.0f;
+    return W4_OK;
+}
+
+// ---------------------------------------------------------------------------------------
+// Prompt attention
+// ---------------------------------------------------------------------------------------
+namespace {
+
+// (head_dim, heads, tokens) view with boxes of 64 elements x box_heads x box_tokens, 128-byte
+// swizzle; elements beyond head_dim and tokens beyond the last read as zero.
+bool make_head_map(CUtensorMap* map, const void* base, bool bf16, int64_t dim, int64_t heads, int64_t tokens,
+                   int64_t head_stride, int64_t token_stride, int box_heads, int box_tokens) {
+    EncodeTiledFn enc = encode_tiled();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)tokens};
+    // the stride of a dimension of one element is never used, but has to be a valid one
+    const cuuint64_t strides[2] = {(cuuint64_t)(heads > 1 ? head_stride : dim) * 2,
+                                   (cuuint64_t)(tokens > 1 ? token_stride : dim) * 2};
+    const cuuint32_t box[3] = {64u, (cuuint32_t)box_heads, (cuuint32_t)box_tokens};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+               const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+w4_status check_attention_sizes(int32_t batch, int32_t heads, int32_t kv_heads, int32_t head_dim, int64_t q_tokens,
+                                int64_t k_tokens) {
+    if (batch < 0 || heads <= 0 || kv_heads <= 0 || heads % kv_heads != 0 || head_dim <= 0 || q_tokens < 0 || k_tokens < 0)
+        return W4_ERR_INVALID_ARG;
+    if (head_dim % 8 != 0 || head_dim > 128 || heads / kv_heads > w4t::kRows) return W4_ERR_UNSUPPORTED;
+    if (q_tokens > INT_MAX / 2 || k_tokens > INT_MAX / 2 || batch > INT_MAX / 2 || heads > 65535) return W4_ERR_UNSUPPORTED;
+    return W4_OK;
+}
+
+template <bool BF16, int DP>
+w4_status launch_attention(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const w4t::AttnParams& p,
+                           long long grid, int dev, cudaStream_t stream) {
+    static std::once_flag flags[kMaxDevices];
+    const auto k = w4t::attention_kernel<BF16, DP>;
+    if (!ensure_smem(k, w4t::Cfg<DP>::bytes, flags, dev)) return W4_ERR_CUDA;
+    // the kernel's register split assumes this many registers a thread at launch
+    static int regs[kMaxDevices];
+    static std::once_flag rflags[kMaxDevices];
+    std::call_once(rflags[dev], [&] {
+        cudaFuncAttributes a;
+        regs[dev] = cudaFuncGetAttributes(&a, k) == cudaSuccess ? a.numRegs : -1;
+    });
+    if (regs[dev] != w4t::kLaunchRegs) return W4_ERR_UNSUPPORTED;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(w4t::kThreads);
+    cfg.dynamicSmemBytes = (size_t)w4t::Cfg<DP>::bytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, k, mq, mk, mv, p) != cudaSuccess) return W4_ERR_CUDA;
+    return launch_status();
+}
+
+}  // namespace
+
+extern "C" size_t w4_prompt_attention_workspace_bytes(int32_t batch, int32_t heads, int32_t kv_heads,
+                                                      int32_t head_dim, int64_t q_tokens, int64_t k_tokens) {
+    if (check_attention_sizes(batch, heads, kv_heads, head_dim, q_tokens, k_tokens) != W4_OK) return 0;
+    return 0;
+}
+
+extern "C" w4_status w4_prompt_attention(const w4_attention* a, w4_dtype dtype, void* workspace,
+                                         size_t workspace_bytes, w4_stream_t stream) {
+    if (!a || (dtype != W4_F16 && dtype != W4_BF16)) return W4_ERR_INVALID_ARG;
+    w4_status st = check_attention_sizes(a->batch, a->heads, a->kv_heads, a->head_dim, a->q_tokens, a->k_tokens);
+    if (st != W4_OK) return st;
+    if (a->causal != 0 && a->causal != 1) return W4_ERR_INVALID_ARG;
+    if (!(a->scale > 0.0f) || !std::isfinite(a->scale)) return W4_ERR_INVALID_ARG;
+    if (!a->cu_seqlens_q && (a->cu_seqlens_k || a->batch != 1)) return W4_ERR_INVALID_ARG;
+    if (a->cu_seqlens_q && !a->cu_seqlens_k && a->q_tokens != a->k_tokens) return W4_ERR_INVALID_ARG;
+    if (a->q_tokens == 0 || a->batch == 0) return W4_OK;
+    if (!a->Q || !a->O || (a->k_tokens > 0 && (!a->K || !a->V))) return W4_ERR_INVALID_ARG;
+    if (!aligned(a->Q, 16) || !aligned(a->K, 16) || !aligned(a->V, 16) || !aligned(a->O, 16) || !aligned(a->lse, 4) ||
+        !aligned(a->cu_seqlens_q, 4) || !aligned(a->cu_seqlens_k, 4))
+        return W4_ERR_INVALID_ARG;
+    const int64_t strides[8] = {a->q_token_stride, a->q_head_stride, a->k_token_stride, a->k_head_stride,
+                                a->v_token_stride, a->v_head_stride, a->o_token_stride, a->o_head_stride};
+    const int64_t counts[8] = {a->q_tokens, a->heads, a->k_tokens, a->kv_heads, a->k_tokens, a->kv_heads, a->q_tokens, a->heads};
+    for (int i = 0; i < 8; ++i) {
+        if (counts[i] <= 1) continue;   // never used
+        if (strides[i] < a->head_dim || strides[i] % 8 != 0) return W4_ERR_INVALID_ARG;
+        if (strides[i] >= (int64_t)1 << 38) return W4_ERR_UNSUPPORTED;   // tensor maps hold 2^40 bytes
+    }
+    const int dev = current_device();
+    if (dev < 0 || dev >= kMaxDevices) return W4_ERR_CUDA;
+    w4t::AttnParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.cu_q = a->cu_seqlens_q;
+    p.cu_k = a->cu_seqlens_k ? a->cu_seqlens_k : a->cu_seqlens_q;
+    p.V = a->V;
+    p.O = a->O;
+    p.lse = a->lse;
+    p.ldv = a->v_token_stride;
+    p.hsv = a->v_head_stride;
+    p.ldo = a->o_token_stride;
+    p.hso = a->o_head_stride;
+    p.batch = a->batch;
+    p.heads = a->heads;
+    p.kv_heads = a->kv_heads;
+    p.group = a->heads / a->kv_heads;
+    p.dim = a->head_dim;
+    p.total_q = (int)a->q_tokens;
+    p.total_k = (int)a->k_tokens;
+    p.tpt = w4t::kRows / p.group;
+    p.causal = a->causal;
+    p.scale = a->scale;
+    p.scale_log2 = a->scale * 1.44269504088896341f;
+    const bool bf16 = dtype == W4_BF16;
+    CUtensorMap mq, mk, mv;
+    // without keys nothing is loaded, but a map needs an address
+    const void* K = a->k_tokens > 0 ? a->K : a->Q;
+    const void* V = a->k_tokens > 0 ? a->V : a->Q;
+    const int64_t kt = std::max<int64_t>(1, a->k_tokens);
+    if (!make_head_map(&mq, a->Q, bf16, a->head_dim, a->heads, a->q_tokens, a->q_head_stride, a->q_token_stride, p.group, p.tpt) ||
+        !make_head_map(&mk, K, bf16, a->head_dim, a->kv_heads, kt, a->k_head_stride, a->k_token_stride, 1, w4t::kKeys) ||
+        !make_head_map(&mv, V, bf16, a->head_dim, a->kv_heads, kt, a->v_head_stride, a->v_token_stride, 1, w4t::kKeys))
+        return W4_ERR_CUDA;
+    // pairs of tiles: no sequence has more than its share rounded up
+    const long long pairs = a->q_tokens / (2 * p.tpt) + std::min<int64_t>(a->batch, a->q_tokens);
+    const long long grid = pairs * a->kv_heads;
+    if (grid > INT_MAX) return W4_ERR_UNSUPPORTED;
+    (void)workspace;
+    (void)workspace_bytes;
+    cudaStream_t strm = as_stream(stream);
+    if (a->head_dim <= 64)
+        return bf16 ? launch_attention<true, 64>(mq, mk, mv, p, grid, dev, strm)
+                    : launch_attention<false, 64>(mq, mk, mv, p, grid, dev, strm);
+    return bf16 ? launch_attention<true, 128>(mq, mk, mv, p, grid, dev, strm)
+                : launch_attention<false, 128>(mq, mk, mv, p, grid, dev, strm);
 }

@@ -374,6 +374,168 @@ w4_status w4a16_gemm_noalloc(const void* X, w4_dtype act_dtype, int64_t M, int64
                              const int32_t* g_idx, int32_t group_size, const float* s_inv,
                              void* Y, w4_dtype out_dtype, w4_stream_t stream);
 
+/*
+ * w4a16_gemm_epi -- w4a16_gemm with bias, activation, gate and residual applied to the fp32
+ * sums, before their one rounding to out_dtype:
+ *   t[m,n] = sum_k X'[m,k] * What[n,k] + bias[n]
+ *   gated == 0:  Y[m,n] = act(t[m,n]) + residual[m,n]                      n < N_out = N
+ *   gated == 1:  Y[m,f] = act(t[m,g(f)]) * t[m,g(f)+8] + residual[m,f]     f < N_out = N/2
+ *                g(f) = 16 * (f / 8) + f % 8
+ * Gated weights (SwiGLU, GeGLU) are two projections packed as one with their rows in
+ * alternating blocks of 8: packed rows 16b .. 16b+7 are gate rows 8b .. 8b+7, packed rows
+ * 16b+8 .. 16b+15 are up rows 8b .. 8b+7 (order the rows of W so before w4_quantize_pack;
+ * scales, zeros and bias follow the packed order).
+ *
+ *   activation  W4_ACT_NONE, W4_ACT_RELU, W4_ACT_SILU x/(1+e^-x), W4_ACT_GELU x Phi(x),
+ *               W4_ACT_GELU_TANH x/2 (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3)))
+ *   bias        device [N] in packed row order, of bias_dtype (fp16, bf16 or fp32), or NULL
+ *   residual    device [M, N_out] of residual_dtype, rows ldr elements apart, or NULL.  It may
+ *               be Y itself (same pointer, ldr == ldy, residual_dtype == out_dtype): each
+ *               element is read before it is written; any other overlap is not allowed
+ *   ldr, ldy    elements between rows of the residual and of Y, at least N_out (0: N_out);
+ *               rows must start on 16-byte boundaries
+ *   g_idx, perm at most one of them: as for w4a16_gemm and w4a16_gemm_perm
+ *   epi         HOST descriptor, read during the call only
+ * Everything else, the workspace (w4a16_workspace_bytes, with perm
+ * w4a16_workspace_bytes_perm; the same buffer may serve both calls on one stream) and its
+ * rules included, is as for w4a16_gemm.  fp16 decode products (M <= 64, no g_idx) multiply
+ * the codes as subnormal fp16 numbers instead of biased ones, so sums differ from
+ * w4a16_gemm's in their last bits (they are nearer the exact value).
+ */
+typedef enum {
+    W4_ACT_NONE = 0,
+    W4_ACT_RELU = 1,
+    W4_ACT_SILU = 2,
+    W4_ACT_GELU = 3,
+    W4_ACT_GELU_TANH = 4
+} w4_activation;
+
+typedef struct {
+    const void* bias;
+    const void* residual;
+    int64_t ldr;
+    int64_t ldy;
+    w4_dtype bias_dtype;
+    w4_dtype residual_dtype;
+    w4_activation activation;
+    int32_t gated;
+} w4_epilogue;
+
+w4_status w4a16_gemm_epi(const void* X, w4_dtype act_dtype, int64_t M, int64_t N, int64_t K,
+                         const uint32_t* qweight, const void* scales, const void* zeros,
+                         const int32_t* g_idx, const int32_t* perm, int32_t group_size,
+                         const float* s_inv, const w4_epilogue* epi, void* Y, w4_dtype out_dtype,
+                         void* workspace, size_t workspace_bytes, w4_stream_t stream);
+
+/*
+ * w4_rope -- rotary positions on the heads of a projection's output (the query and key heads
+ * of a fused qkv projection are one run of heads of each row).  For token t, head h and pair
+ * i < rot_dim/2, with phi = positions[t] * inv_freq[i]:
+ *   Y[t,h,a_i] = mscale * (X[t,h,a_i] cos phi - X[t,h,b_i] sin phi)
+ *   Y[t,h,b_i] = mscale * (X[t,h,b_i] cos phi + X[t,h,a_i] sin phi)
+ *   interleaved == 0: a_i = i, b_i = i + rot_dim/2;  interleaved == 1: a_i = 2i, b_i = 2i+1
+ *   elements rot_dim .. head_dim-1 are copied
+ * The angle is taken in fp64, sine, cosine and the rotation in fp32, rounded once.
+ *   X           device; element d of head h of token t is X[t*x_token_stride +
+ *               h*x_head_stride + d] (strides in elements); fp16, bf16 or fp32 (dtype)
+ *   Y           device, the same type, strides of its own.  Y == X with equal strides rotates
+ *               in place; any other overlap is not allowed
+ *   positions   device int32 [tokens];  inv_freq  device fp64 [rot_dim/2]
+ *   rot_dim     even, 2 .. head_dim, at most 512;  mscale finite
+ * Any stride and alignment of whole elements works; 16-byte alignment of the pointers and
+ * strides, with head_dim and rot_dim/2 multiples of 16 bytes, is faster.  tokens == 0 or
+ * heads == 0 is a no-op.  Asynchronous on `stream`; no workspace.
+ */
+w4_status w4_rope(const void* X, w4_dtype dtype, int64_t tokens, int32_t heads, int32_t head_dim,
+                  int64_t x_token_stride, int64_t x_head_stride, const int32_t* positions,
+                  const double* inv_freq, int32_t rot_dim, float mscale, int32_t interleaved,
+                  void* Y, int64_t y_token_stride, int64_t y_head_stride, w4_stream_t stream);
+
+/*
+ * w4_rope_freqs -- the frequencies of w4_rope on the HOST: inv_freq[i] = theta^(-2i/rot_dim),
+ * i < rot_dim/2, stretched for contexts longer than the `context` tokens a model was trained
+ * on by `factor` (> 0), and the factor *mscale for w4_rope:
+ *   W4_ROPE_PLAIN   unchanged, mscale 1 (factor, context, lo, hi unused)
+ *   W4_ROPE_LINEAR  inv_freq / factor, mscale 1
+ *   W4_ROPE_BASE    theta * factor^(rot_dim/(rot_dim-2)) as the base, mscale 1
+ *   W4_ROPE_BANDS   by wavelength w = 2 pi / inv_freq: unchanged where w < context/hi, divided
+ *                   by factor where w > context/lo, between them a blend by context/w that is
+ *                   linear from lo to hi; mscale 1; 0 < lo < hi (common: 1, 4)
+ *   W4_ROPE_RAMP    (the ramp over pair indices of the YaRN method) unchanged below the pair
+ *                   that turns hi times within the context, divided by factor above the pair
+ *                   that turns lo times, linear between; mscale 0.1 ln(factor) + 1 for
+ *                   factor > 1, else 1; 0 < lo < hi (common: 1, 32)
+ */
+typedef enum {
+    W4_ROPE_PLAIN = 0,
+    W4_ROPE_LINEAR = 1,
+    W4_ROPE_BASE = 2,
+    W4_ROPE_BANDS = 3,
+    W4_ROPE_RAMP = 4
+} w4_rope_scaling;
+
+w4_status w4_rope_freqs(int32_t rot_dim, double theta, w4_rope_scaling scaling, double factor,
+                        double context, double lo, double hi, double* inv_freq, float* mscale);
+
+/*
+ * w4_prompt_attention -- softmax attention over a packed batch of prompts, or of the next
+ * tokens of sequences over their earlier keys, with grouped heads:
+ *   O[t,h] = sum_j p_j V[j,hk],  p = softmax_j(scale * Q[t,h] . K[j,hk]),  hk = h / (heads/kv_heads)
+ * over the keys j of the token's own sequence b that its position sees.  Sequence b has
+ * query tokens cu_seqlens_q[b] .. cu_seqlens_q[b+1]-1 (nq of them) and keys
+ * cu_seqlens_k[b] .. cu_seqlens_k[b+1]-1 (nk); query i of it sees keys
+ *   causal == 1:  j <= i + nk - nq   (the last query sees every key)
+ *   causal == 0:  every key.
+ * A query that sees no key (nk == 0, or causal with nk < nq) gets O = 0 and lse = -inf.
+ * Scores, softmax statistics and sums are fp32; the weights p are rounded to the input type
+ * for their product with V; O is rounded once.  Only seen keys matter: rows of K and V behind
+ * a sequence's end and later positions may hold anything, NaN and infinities included.
+ *
+ *   a         HOST descriptor, read during the call only:
+ *     Q, K, V, O  device, dtype fp16 or bf16; element d of head h of token t at
+ *                 t*token_stride + h*head_stride + d (strides in elements, multiples of 8;
+ *                 pointers 16-byte aligned).  O must not overlap Q, K or V
+ *     lse         device fp32 [q_tokens, heads] log of the softmax sum (natural), or NULL
+ *     cu_seqlens_q, cu_seqlens_k  device int32 [batch+1], ascending.  cu_seqlens_k NULL: the
+ *                 same as cu_seqlens_q; both NULL: one sequence (batch == 1) of all tokens.
+ *                 Bounds outside [0, q_tokens] or [0, k_tokens] are clamped and reported as
+ *                 W4_ERR_DEVICE_ARG by w4_check_device_error()
+ *     q_tokens, k_tokens  rows of Q and O, and of K and V.  Rows behind the last sequence are
+ *                 not read for any result and their O and lse stay as they were
+ *     heads       a multiple of kv_heads, at most 128 of them to a key head
+ *     head_dim    a multiple of 8, 8 .. 128
+ *     scale       > 0, finite (commonly 1/sqrt(head_dim))
+ *   workspace device scratch of at least w4_prompt_attention_workspace_bytes(...) bytes,
+ *             256-byte aligned, of any content; calls that may overlap on the GPU need
+ *             separate ones.  NULL when that is 0
+ * q_tokens == 0 is a no-op.  Asynchronous on `stream`; may be captured into a graph.
+ */
+typedef struct {
+    const void* Q;
+    const void* K;
+    const void* V;
+    void* O;
+    float* lse;
+    const int32_t* cu_seqlens_q;
+    const int32_t* cu_seqlens_k;
+    int64_t q_tokens, k_tokens;
+    int64_t q_token_stride, q_head_stride;
+    int64_t k_token_stride, k_head_stride;
+    int64_t v_token_stride, v_head_stride;
+    int64_t o_token_stride, o_head_stride;
+    int32_t batch, heads, kv_heads, head_dim;
+    float scale;
+    int32_t causal;
+} w4_attention;
+
+w4_status w4_prompt_attention(const w4_attention* a, w4_dtype dtype, void* workspace,
+                              size_t workspace_bytes, w4_stream_t stream);
+
+/* Bytes of workspace w4_prompt_attention needs on the current device (0 when it needs none,
+ * and on invalid sizes). */
+size_t w4_prompt_attention_workspace_bytes(int32_t batch, int32_t heads, int32_t kv_heads,
+                                           int32_t head_dim, int64_t q_tokens, int64_t k_tokens);
+
 /* Bytes of workspace w4a16_gemm needs for these sizes on the current device
  * (0 on invalid sizes). */
 size_t w4a16_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t group_size);
