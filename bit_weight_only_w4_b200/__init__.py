@@ -13,6 +13,7 @@ is missing or a call fails, an exception is raised.
 """
 import ctypes
 import os
+import struct
 import threading
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -107,7 +108,7 @@ def lib():
         L.w4_rope.restype = st
         L.w4_rope_freqs.argtypes = [i32, f64, st, f64, f64, f64, f64, ctypes.POINTER(f64), ctypes.POINTER(f32)]
         L.w4_rope_freqs.restype = st
-        L.w4_prompt_attention.argtypes = [ctypes.POINTER(Attention), st, vp, sz, vp]
+        L.w4_prompt_attention.argtypes = [vp, st, vp, sz, vp]   # w4_attention: an Attention by reference, or its bytes
         L.w4_prompt_attention.restype = st
         L.w4_prompt_attention_workspace_bytes.argtypes = [i32, i32, i32, i32, i64, i64]
         L.w4_prompt_attention_workspace_bytes.restype = sz
@@ -140,6 +141,10 @@ class Attention(ctypes.Structure):
                 + [("scale", ctypes.c_float), ("causal", ctypes.c_int32)])
 
 
+_ATTENTION = struct.Struct("@7P10q4ifi")   # the same, packed
+assert _ATTENTION.size == ctypes.sizeof(Attention)
+
+
 # ---------------------------------------------------------------- marshalling helpers
 def _torch():
     import torch
@@ -163,9 +168,32 @@ def _ptr(t):
 
 
 def _stream_handle(stream, device):
+    # the current stream's handle without building a torch.cuda.Stream (a call per layer and token)
+    return stream.cuda_stream if stream is not None else _torch()._C._cuda_getCurrentRawStream(device.index)
+
+
+_sizes = {}
+
+
+def _workspace_size(index, fn, *args):
+    """What a w4_*_workspace_bytes function of the library says for these sizes on device
+    `index`, remembered (it depends on nothing else)."""
+    key = (index, fn.__name__, args)
+    need = _sizes.get(key)
+    if need is None:
+        if len(_sizes) >= 4096:
+            _sizes.clear()
+        need = _sizes[key] = _on_device(index, fn, *args)
+    return need
+
+
+def _on_device(index, fn, *args):
+    """fn(*args) with CUDA device `index` current (the common case: it is already)."""
     torch = _torch()
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    return ctypes.c_void_p(s.cuda_stream)
+    if torch._C._cuda_getDevice() == index:
+        return fn(*args)
+    with torch.cuda.device(index):
+        return fn(*args)
 
 
 def _check(status, what):
@@ -650,22 +678,17 @@ def gated_rows(F, device=None):
     return torch.cat([f, f + F], 1).reshape(-1)
 
 
-def _rows_of(t, name, dtypes, shape, dev):
-    """A matrix of the given shape whose elements are contiguous within rows (rows may be
-    further apart); returns its row stride."""
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if t.device != dev:
-        raise ValueError("tensors are on different devices")
-    if t.shape[0] <= 1:
-        if t.shape[1] > 1 and t.stride(1) != 1:
-            raise ValueError(f"{name}: elements of a row must be contiguous")
-        return t.shape[1]
-    if (t.shape[1] > 1 and t.stride(1) != 1) or t.stride(0) < t.shape[1]:
+def _rows_of(t, name, rows, cols):
+    """The row stride of a [rows, cols] matrix whose elements are contiguous within rows
+    (rows may be further apart)."""
+    if t.dtype not in _dtypes()[:3]:
+        raise TypeError(f"{name} must be torch.float16, torch.bfloat16 or torch.float32, not {t.dtype}")
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name} must have shape {(rows, cols)}, not {tuple(t.shape)}")
+    ld, one = t.stride()
+    if (cols > 1 and one != 1) or (rows > 1 and ld < cols):
         raise ValueError(f"{name}: elements of a row must be contiguous, and rows must not overlap")
-    return t.stride(0)
+    return ld if rows > 1 else cols
 
 
 def w4a16_gemm_epi(X, qweight, scales, zeros, group_size=128, bias=None, activation=None, gated=False,
@@ -687,58 +710,60 @@ def w4a16_gemm_epi(X, qweight, scales, zeros, group_size=128, bias=None, activat
     act = _ACTIVATIONS.get(activation)
     if act is None:
         raise ValueError(f"unknown activation {activation!r} ({', '.join(k for k in _ACTIVATIONS if k)})")
-    floats = _dtypes()[:3]
-    if bias is not None and (bias.dtype not in floats or bias.numel() != N):
-        _expect(bias, "bias", floats, numel=N)
+    if bias is not None:
+        _expect(bias, "bias", _dtypes()[:3], numel=N)
     dev = _need_cuda(X, qweight, scales, zeros, g_idx, s_inv, bias, workspace, perm)
     n_out = N // 2 if gated else N
+    xt = X.dtype
     if Y is None:
-        Y = torch.empty(M, n_out, dtype=out_dtype or X.dtype, device=dev)
+        yt = out_dtype or xt
+        Y = torch.empty((M, n_out), dtype=yt, device=dev)
         ldy = n_out
     else:
-        if out_dtype is not None and out_dtype != Y.dtype:
-            raise TypeError(f"Y is {Y.dtype}, out_dtype {out_dtype}")
-        ldy = _rows_of(Y, "Y", floats, (M, n_out), dev)
-    e = Epilogue()
-    e.ldy = ldy
-    e.activation = act
-    e.gated = 1 if gated else 0
-    if bias is not None:
-        e.bias = bias.data_ptr()
-        e.bias_dtype = _dtype_code(bias.dtype)
-    if residual is not None:
-        e.ldr = _rows_of(residual, "residual", floats, (M, n_out), dev)
-        e.residual = residual.data_ptr()
-        e.residual_dtype = _dtype_code(residual.dtype)
-    with _DeviceGuard(dev):
-        L = lib()
-        if workspace is None and M > 0:
-            need = (L.w4a16_workspace_bytes if perm is None else L.w4a16_workspace_bytes_perm)(M, N, K, int(group_size))
-            if need > 0:
-                workspace = workspace_for(dev, need)
-        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        st = L.w4a16_gemm_epi(_ptr(X), _dtype_code(X.dtype), M, N, K, _ptr(qweight), _ptr(scales), _ptr(zeros),
-                              _ptr(g_idx), _ptr(perm), int(group_size), _ptr(s_inv), e, _ptr(Y),
-                              _dtype_code(Y.dtype), _ptr(workspace), ws_bytes, _stream_handle(stream, dev))
-    _check(st, "w4a16_gemm_epi")
+        yt = Y.dtype
+        if out_dtype is not None and out_dtype != yt:
+            raise TypeError(f"Y is {yt}, out_dtype {out_dtype}")
+        ldy = _rows_of(Y, "Y", M, n_out)
+    ldr = 0 if residual is None else _rows_of(residual, "residual", M, n_out)
+    if Y.device != dev or (residual is not None and residual.device != dev):
+        raise ValueError("tensors are on different devices")
+    e = Epilogue(_ptr(bias), _ptr(residual), ldr, ldy, 0 if bias is None else _dtype_code(bias.dtype),
+                 0 if residual is None else _dtype_code(residual.dtype), act, 1 if gated else 0)
+    L = lib()
+    if workspace is None and M > 0:
+        need = _workspace_size(dev.index, L.w4a16_workspace_bytes if perm is None else L.w4a16_workspace_bytes_perm,
+                               M, N, K, group_size)
+        if need > 0:
+            workspace = workspace_for(dev, need)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    st = _on_device(dev.index, L.w4a16_gemm_epi, X.data_ptr(), _dtype_code(xt), M, N, K, qweight.data_ptr(),
+                    scales.data_ptr(), _ptr(zeros), _ptr(g_idx), _ptr(perm), group_size, _ptr(s_inv), e, Y.data_ptr(),
+                    _dtype_code(yt), _ptr(workspace), ws_bytes, _stream_handle(stream, dev))
+    if st:
+        raise W4Error(st, "w4a16_gemm_epi")
     return Y
 
 
-def _heads_of(t, name, dev=None, dtype=None, shape=None):
-    """A [tokens, heads, head_dim] CUDA tensor (a view with contiguous head elements)."""
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [tokens, heads, head_dim], not of shape {tuple(t.shape)}")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if not t.is_cuda:
-        raise ValueError("all tensors must be CUDA tensors (there is no CPU path)")
-    if dev is not None and t.device != dev:
-        raise ValueError("tensors are on different devices")
-    if t.shape[2] > 1 and t.stride(2) != 1:
+def _heads_of(t, name):
+    """(shape, strides) of a [tokens, heads, head_dim] CUDA tensor (a view with contiguous
+    head elements)."""
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim], not of shape {tuple(shape)}")
+    if strides[2] != 1 and shape[2] > 1:
         raise ValueError(f"{name}: elements of a head must be contiguous")
-    return t.stride(0), t.stride(1)
+    return shape, strides
+
+
+def _cuda_index(*tensors):
+    """The index of the one CUDA device that the tensors (or None) are on."""
+    index = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != index:
+            raise ValueError("tensors are on different devices")
+    if index < 0:
+        raise ValueError("all tensors must be CUDA tensors (there is no CPU path)")
+    return index
 
 
 def w4_rope_freqs(rot_dim, theta=10000.0, scaling=None, factor=1.0, context=8192, lo=1.0, hi=4.0, device=None):
@@ -766,26 +791,32 @@ def w4_rope(X, positions, inv_freq, interleaved=False, mscale=1.0, Y=None, strea
     inv_freq[i], as pairs (i, i + len(inv_freq)) or, interleaved, (2i, 2i+1).  positions int32
     [tokens], inv_freq float64.  Y=X rotates in place; without Y a new tensor is returned."""
     torch = _torch()
-    sx = _heads_of(X, "X")
-    dev = X.device
-    T, H, D = X.shape
-    _expect(positions, "positions", (torch.int32,), shape=(T,))
-    _expect(inv_freq, "inv_freq", (torch.float64,))
-    if inv_freq.dim() != 1 or 2 * inv_freq.shape[0] > D or inv_freq.shape[0] == 0:
-        raise ValueError(f"inv_freq must hold 1 .. {D // 2} frequencies, not {tuple(inv_freq.shape)}")
-    _need_cuda(positions, inv_freq)
-    if positions.device != dev or inv_freq.device != dev:
-        raise ValueError("tensors are on different devices")
+    shape, sx = _heads_of(X, "X")
+    T, H, D = shape
+    if positions.dtype is not torch.int32 or positions.shape != (T,) or not positions.is_contiguous():
+        _expect(positions, "positions", (torch.int32,), shape=(T,))
+        raise ValueError("positions must be contiguous")
+    if inv_freq.dtype is not torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        _expect(inv_freq, "inv_freq", (torch.float64,))
+        raise ValueError("inv_freq must be a contiguous vector")
+    rot = 2 * inv_freq.shape[0]
+    if rot > D or rot == 0:
+        raise ValueError(f"inv_freq must hold 1 .. {D // 2} frequencies, not {rot // 2}")
+    xt = X.dtype
     if Y is None:
-        Y = torch.empty(T, H, D, dtype=X.dtype, device=dev)
+        index = _cuda_index(X, positions, inv_freq)
+        Y = torch.empty(shape, dtype=xt, device=X.device)
         sy = (H * D, D)
     else:
-        sy = _heads_of(Y, "Y", dev, X.dtype, X.shape)
-    with _DeviceGuard(dev):
-        st = lib().w4_rope(X.data_ptr(), _dtype_code(X.dtype), T, H, D, sx[0], sx[1], positions.data_ptr(),
-                           inv_freq.data_ptr(), 2 * inv_freq.shape[0], float(mscale), 1 if interleaved else 0,
-                           Y.data_ptr(), sy[0], sy[1], _stream_handle(stream, dev))
-    _check(st, "w4_rope")
+        index = _cuda_index(X, positions, inv_freq, Y)
+        ys, sy = _heads_of(Y, "Y")
+        if Y.dtype is not xt or ys != shape:
+            _expect(Y, "Y", (xt,), shape=shape)
+    st = _on_device(index, lib().w4_rope, X.data_ptr(), _dtype_code(xt), T, H, D, sx[0], sx[1], positions.data_ptr(),
+                    inv_freq.data_ptr(), rot, mscale, 1 if interleaved else 0, Y.data_ptr(), sy[0], sy[1],
+                    torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
+    if st:
+        raise W4Error(st, "w4_rope")
     return Y
 
 
@@ -807,47 +838,55 @@ def w4_prompt_attention(Q, K, V, cu_seqlens=None, cu_seqlens_k=None, causal=True
     with return_lse also lse float32 [q_tokens, heads].
 
     Where a call needs scratch (w4_prompt_attention_workspace_bytes) and passes none, it is
-    allocated on the current stream; pass `workspace` when `stream` is another one."""
+    allocated for this call on the stream it runs on."""
     torch = _torch()
-    sq, sk, sv = _heads_of(Q, "Q"), _heads_of(K, "K"), _heads_of(V, "V")
-    dt, dev = Q.dtype, Q.device
+    (Tq, H, D), sq = _heads_of(Q, "Q")
+    ks, sk = _heads_of(K, "K")
+    vs, sv = _heads_of(V, "V")
+    dt = Q.dtype
     if dt is not torch.float16 and dt is not torch.bfloat16:
         raise TypeError(f"Q must be torch.float16 or torch.bfloat16, not {dt}")
-    if K.dtype != dt or V.dtype != dt:
+    if K.dtype is not dt or V.dtype is not dt:
         raise TypeError("Q, K and V must have one dtype")
-    Tq, H, D = Q.shape
-    Tk, Hk = K.shape[0], K.shape[1]
-    if K.shape != V.shape or K.shape[2] != D:
-        raise ValueError(f"K and V must be [k_tokens, kv_heads, {D}], not {tuple(K.shape)} and {tuple(V.shape)}")
-    if K.device != dev or V.device != dev:
-        raise ValueError("tensors are on different devices")
+    if ks != vs or ks[2] != D:
+        raise ValueError(f"K and V must be [k_tokens, kv_heads, {D}], not {tuple(ks)} and {tuple(vs)}")
+    Tk, Hk = ks[0], ks[1]
     batch = 1
+    if cu_seqlens is not None:
+        batch = cu_seqlens.shape[0] - 1 if cu_seqlens.dim() == 1 else -1
     for cu, name in ((cu_seqlens, "cu_seqlens"), (cu_seqlens_k, "cu_seqlens_k")):
-        if cu is None:
-            continue
-        if cu.dtype is not torch.int32:
-            raise TypeError(f"{name} must be torch.int32, not {cu.dtype}")
-        if cu.dim() != 1 or cu.shape[0] < 1 or not cu.is_contiguous() or cu.device != dev:
-            raise ValueError(f"{name} must be a contiguous vector of batch+1 bounds on {dev}")
-        batch = cu.shape[0] - 1
-    if cu_seqlens_k is not None and (cu_seqlens is None or cu_seqlens.shape != cu_seqlens_k.shape):
-        raise ValueError("cu_seqlens_k needs a cu_seqlens of the same length")
+        if cu is not None:
+            if cu.dtype is not torch.int32:
+                raise TypeError(f"{name} must be torch.int32, not {cu.dtype}")
+            if cu_seqlens is None or batch < 0 or cu.shape != (batch + 1,) or not cu.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous vector of batch+1 bounds, cu_seqlens_k with a "
+                                 "cu_seqlens of the same length")
+    index = _cuda_index(Q, K, V, cu_seqlens, cu_seqlens_k, O, workspace)
+    dev = Q.device
     if O is None:
-        O = torch.empty(Tq, H, D, dtype=dt, device=dev)
+        O = torch.empty((Tq, H, D), dtype=dt, device=dev)
         so = (H * D, D)
     else:
-        so = _heads_of(O, "O", dev, dt, Q.shape)
-    lse = torch.empty(Tq, H, dtype=torch.float32, device=dev) if return_lse else None
-    a = Attention(Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), _ptr(lse), _ptr(cu_seqlens),
-                  _ptr(cu_seqlens_k), Tq, Tk, sq[0], sq[1], sk[0], sk[1], sv[0], sv[1], so[0], so[1],
-                  batch, H, Hk, D, D ** -0.5 if scale is None else float(scale), 1 if causal else 0)
-    with _DeviceGuard(dev):
-        L = lib()
-        if workspace is None:
-            need = L.w4_prompt_attention_workspace_bytes(batch, H, Hk, D, Tq, Tk)
-            if need > 0:
+        os_, so = _heads_of(O, "O")
+        if O.dtype is not dt or os_ != (Tq, H, D):
+            _expect(O, "O", (dt,), shape=(Tq, H, D))
+    lse = torch.empty((Tq, H), dtype=torch.float32, device=dev) if return_lse else None
+    # w4_attention, packed at once (a ctypes structure of 24 fields takes longer to fill)
+    a = _ATTENTION.pack(Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), 0 if lse is None else lse.data_ptr(),
+                        0 if cu_seqlens is None else cu_seqlens.data_ptr(),
+                        0 if cu_seqlens_k is None else cu_seqlens_k.data_ptr(), Tq, Tk, sq[0], sq[1], sk[0], sk[1],
+                        sv[0], sv[1], so[0], so[1], batch, H, Hk, D, D ** -0.5 if scale is None else scale,
+                        1 if causal else 0)
+    L = lib()
+    if workspace is None:
+        need = _workspace_size(index, L.w4_prompt_attention_workspace_bytes, batch, H, Hk, D, Tq, Tk)
+        if need > 0:
+            # of the stream that uses it, so that its next use is ordered behind this call
+            with torch.cuda.stream(stream):
                 workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        st = L.w4_prompt_attention(a, _dtype_code(dt), _ptr(workspace), ws_bytes, _stream_handle(stream, dev))
-    _check(st, "w4_prompt_attention")
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    st = _on_device(index, L.w4_prompt_attention, a, _dtype_code(dt), _ptr(workspace), ws_bytes,
+                    torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
+    if st:
+        raise W4Error(st, "w4_prompt_attention")
     return (O, lse) if return_lse else O

@@ -10,9 +10,15 @@
 // A tile's 128 rows are tokens x the G query heads that share a key head (row = token * G +
 // head in the group), so a K or V tile in shared memory serves G heads, the causal
 // diagonal is only 128 / G tokens wide, and one token of many sequences still fills rows.
-// A CTA (one per SM) takes a pair of tiles, 384 threads:
-//   warps 0-3, 4-7  softmax of tile A, B: a thread owns one row of S (tensor memory lane);
-//   warp 8          TMA: Q of both tiles, then K and V tiles of 128 keys through a ring;
+// An item of work is a pair of tiles A, B of one sequence and key head over the same key
+// blocks, or (when pairs would leave SMs idle) one tile, whose even key blocks are A's and
+// odd ones B's: two partial softmaxes of the same rows, joined at the item's end straight
+// from tensor memory.  One CTA an SM, 384 threads, takes items until there are none; the
+// roles run ahead of one another through barriers, so the loads and the first products of
+// the next item overlap the end of this one:
+//   warps 0-3, 4-7  softmax of A, B: a thread owns one row of S (tensor memory lane), then the
+//                   item's output;
+//   warp 8          finds the items, loads Q, then K and V tiles of 128 keys through a ring;
 //   warp 9          issues tcgen05.mma: S = Q K^T (128 x 128), O += P V; the two tiles take
 //                   turns, so one tile's softmax runs beside the other's products;
 //   warps 10-11     make the V tiles of masked key blocks finite (below).
@@ -21,11 +27,21 @@
 // by 8 (in powers of two): sums grow by at most 2^8, nothing is lost in fp32, and O is
 // rescaled a few times a row instead of once a key block.
 //
+// Two ways to share the work:
+//   items    longest first, one CTA an item; a running CTA takes the place of one that has
+//            not started (cluster launch control), so the hardware balances their lengths;
+//   ranges   (few tokens over many keys) all key blocks of all items in one list, cut into
+//            equal runs, one a CTA: every SM reads the same number of keys whatever the
+//            sequences' lengths.  An item that a cut divides is written as partial outputs
+//            (at most two a CTA) and joined by combine_kernel.
+//
 // Masked keys: their scores are replaced (not shifted) before the maximum.  A masked key's
 // P is 0, but 0 * V is NaN for an infinite or NaN V, so in key blocks that hold a masked
 // key the spare warps zero V's rows behind the sequence's end and its other non-finite
-// values, and rows that do see such a value get it added in the epilogue.
+// values, and rows that do see such a value get it added to their output.
 #pragma once
+#include <climits>
+
 #include "w4_common.cuh"
 #include "w4_prefill.cuh"
 
@@ -38,43 +54,60 @@ constexpr int kRegsSoftmax = 208, kRegsOther = 88, kLaunchRegs = 168;
 static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * kLaunchRegs, "register split");
 constexpr float kLazy = 8.0f;   // powers of two by which a row may pass its reference maximum
 
+constexpr int kItems = 3;       // items the producer may be ahead of the output, plus one
+
 template <int DP>
 struct Cfg {
     static constexpr int q_tile = kRows * DP * 2;
     static constexpr int kv_tile = kKeys * DP * 2;
-    static constexpr int stages = DP == 128 ? 5 : 10;
+    static constexpr int stages = DP == 128 ? 4 : 8;
     static constexpr int q = 0;
     static constexpr int ring = 2 * q_tile;
-    static constexpr int bars = ring + stages * kv_tile;
-    // full, empty, raw, fixed (per stage); q full; per tile: s full, p full, o done; all done
-    static constexpr int nbars = 4 * stages + 1 + 3 * 2 + 1;
-    static constexpr int misc = bars + nbars * 8;
-    static constexpr int bytes = misc + 64 + 1024;
+    static constexpr int out = ring + stages * kv_tile;     // 4 KB a softmax warp
+    static constexpr int bars = out + 8 * 4096;
+    // full, empty, raw, fixed (per stage); item full, empty; q full, empty; per tile: s full,
+    // p full, o done; next item; all done; both ready, read
+    static constexpr int nbars = 4 * stages + 2 * kItems + 2 + 3 * 2 + 4;
+    static constexpr int next = (bars + nbars * 8 + 15) / 16 * 16;   // cluster launch control's answer
+    static constexpr int items = next + 16;
+    static constexpr int misc = items + kItems * 64;
+    static constexpr int stats = q + q_tile;   // one tile: (m, l) of A's and B's rows, where Q of tile B would be
+    static constexpr int bytes = misc + 16 + 1024;
     static_assert(bytes <= 227 * 1024, "shared memory");
 };
 
 struct AttnParams {
     const int32_t* cu_q;     // [batch + 1]
     const int32_t* cu_k;     // [batch + 1]
-    const void* V;           // for the epilogue's repair only
+    const void* V;           // for the output's repair only
     void* O;
     float* lse;              // [total_q, heads] or null
+    float* part_o;           // ranges: partial outputs [2 a CTA][128 rows][dim] fp32; null for items
+    float* part_lse;         // [2 a CTA][128 rows]
     long long ldv, hsv, ldo, hso;
     int batch, heads, kv_heads, group, dim;
     int total_q, total_k;
     int tpt;                 // tokens of a tile: 128 / group
+    int tiles;               // tiles of an item: 1 or 2
+    int ctas;                // ranges: their number
     int causal;
     float scale, scale_log2; // scale, scale * log2 e
 };
 
-// One CTA's work: a pair of tiles of one sequence and key head.
+// An item (or the part of one in a CTA's range): tiles of one sequence and key head.
 struct Work {
     int valid;
     int q0, nq;      // first token of the sequence, its tokens
     int k0, nk;      // first key of the sequence, its keys
-    int tok;         // first token (in the sequence) of the pair
+    int tok;         // first token (in the sequence) of the item
     int hk;          // key head
+    int part;        // partial output it writes, or -1: the output itself
+    int b0;          // first key block
+    int nb0, nb1;    // key blocks of A, of B (one tile: together the item's, alternately)
+    int mfirst;      // the item's blocks from this one on hold a key that some row does not see
+    int poison;      // set when a non-finite value was taken out of V
 };
+static_assert(sizeof(Work) <= 64, "item slot");
 
 // First element and length of sequence b; bounds outside [0, total] are clamped (bad).  A
 // null cu is one sequence of everything.
@@ -91,88 +124,190 @@ W4_DEV void seq_bounds(const int32_t* cu, int total, int b, int& s, int& n, bool
     bad |= a < 0 || e < a || e > total;
 }
 
-// Pairs of all sequences in descending order of their index in the sequence (with causal
-// masks, of their cost), so the long ones start first: pair `idx` by a search for the
-// level p with f(p) > idx >= f(p + 1), f(p) = sum_b max(0, pairs of b - p).  Run by one warp.
-W4_DEV Work find_work(const AttnParams& p, int idx, int hk, int lane) {
-    const int tp = 2 * p.tpt;
-    auto count = [&](int level) {
-        int c = 0;
-        for (int b = lane; b < p.batch; b += 32) {
-            int s, n;
-            bool bad = false;
-            seq_bounds(p.cu_q, p.total_q, b, s, n, bad);
-            c += max(0, (n + tp - 1) / tp - level);
-        }
-        return __reduce_add_sync(0xffffffffu, c);
+// Tiles x rows of an item, as tokens.
+W4_DEV int item_tokens(const AttnParams& p) { return p.tiles * p.tpt; }
+
+// Fills in what tile `tok` of a sequence does over its key blocks [from, to).
+W4_DEV void fill_work(const AttnParams& p, Work& w, int from, int to) {
+    // keys that some row of a tile sees, and that every row of the item sees
+    auto sees = [&](int last) { return p.causal ? max(0, min(w.nk, last + 1 + w.nk - w.nq)) : w.nk; };
+    auto blocks = [&](int t0) {   // of the tile that starts at token t0
+        return t0 >= w.nq ? 0 : (sees(min(t0 + p.tpt, w.nq) - 1) + kKeys - 1) / kKeys;
     };
-    Work w = {};
-    if (count(0) <= idx) return w;
-    int lo = 0, hi = p.total_q / tp + 1;   // f(lo) > idx >= f(hi)
-    while (hi - lo > 1) {
-        const int mid = lo + (hi - lo) / 2;
-        if (count(mid) > idx) lo = mid;
-        else hi = mid;
-    }
-    int rank = idx - count(lo + 1);   // among the sequences with more than lo pairs
-    for (int b0 = 0; b0 < p.batch; b0 += 32) {
-        const int b = b0 + lane;
-        int s = 0, n = 0;
-        bool bad = false;
-        if (b < p.batch) seq_bounds(p.cu_q, p.total_q, b, s, n, bad);
-        const unsigned has = __ballot_sync(0xffffffffu, (n + tp - 1) / tp > lo);
-        const int c = __popc(has);
-        if (rank >= c) {
-            rank -= c;
-            continue;
-        }
-        const int src = __fns(has, 0, rank + 1);
-        w.valid = 1;
-        w.q0 = __shfl_sync(0xffffffffu, s, src);
-        w.nq = __shfl_sync(0xffffffffu, n, src);
-        bad = false;
-        seq_bounds(p.cu_k, p.total_k, b0 + src, w.k0, w.nk, bad);
-        w.tok = lo * tp;
-        w.hk = hk;
-        break;
-    }
-    return w;
+    const int n0 = max(0, min(blocks(w.tok), to) - from);
+    w.valid = 1;
+    w.b0 = from;
+    w.nb0 = p.tiles == 2 ? n0 : (n0 + 1) / 2;
+    w.nb1 = p.tiles == 2 ? max(0, min(blocks(w.tok + p.tpt), to) - from) : n0 / 2;
+    w.mfirst = max(0, sees(w.tok) / kKeys - from);
 }
 
-// Keys (from the sequence's first) that some row of tile x sees, and that every row sees.
-W4_DEV int tile_keys(const AttnParams& p, const Work& w, int x) {
-    const int t0 = w.tok + x * p.tpt, t1 = min(t0 + p.tpt, w.nq);
-    if (t0 >= w.nq) return 0;
-    return p.causal ? max(0, min(w.nk, t1 + w.nk - w.nq)) : w.nk;
-}
-W4_DEV int common_keys(const AttnParams& p, const Work& w) {
-    return p.causal ? max(0, min(w.nk, w.tok + 1 + w.nk - w.nq)) : w.nk;
-}
+// Finds items, by one warp.  The items of all sequences are taken in descending index in
+// their sequence (with causal masks, descending cost): item `idx` is at the level v with
+// f(v) > idx >= f(v + 1), f(v) = sum_b max(0, items of b - v), found by bisection.  Up to 32
+// sequences keep their counts in the lanes.
+struct Finder {
+    int mine, top;   // items of this lane's sequence, the most of any sequence
+    W4_DEV static int items_of(const AttnParams& p, int b) {
+        int s, n;
+        bool bad = false;
+        seq_bounds(p.cu_q, p.total_q, b, s, n, bad);
+        return (n + item_tokens(p) - 1) / item_tokens(p);
+    }
+    W4_DEV void start(const AttnParams& p, int lane) {
+        mine = 0;
+        int most = 0;
+        for (int b = lane; b < p.batch; b += 32) {
+            const int n = items_of(p, b);
+            if (b == lane) mine = n;
+            most = max(most, n);
+        }
+        top = __reduce_max_sync(0xffffffffu, most);
+    }
+    W4_DEV int count(const AttnParams& p, int level, int lane) const {
+        int c = lane < p.batch ? max(0, mine - level) : 0;
+        for (int b = lane + 32; b < p.batch; b += 32) c += max(0, items_of(p, b) - level);
+        return __reduce_add_sync(0xffffffffu, c);
+    }
+    W4_DEV Work find(const AttnParams& p, int item, int lane) const {
+        Work w = {};
+        const int idx = item / p.kv_heads;
+        if (count(p, 0, lane) <= idx) return w;
+        int lo = 0, hi = top;   // f(lo) > idx >= f(hi)
+        while (hi - lo > 1) {
+            const int mid = lo + (hi - lo) / 2;
+            if (count(p, mid, lane) > idx) lo = mid;
+            else hi = mid;
+        }
+        int rank = idx - count(p, lo + 1, lane);   // among the sequences with more than lo items
+        int b = 0;
+        for (int b0 = 0; b0 < p.batch; b0 += 32) {
+            const int n = b0 + lane < p.batch ? (b0 == 0 ? mine : items_of(p, b0 + lane)) : 0;
+            unsigned has = __ballot_sync(0xffffffffu, n > lo);
+            const int c = __popc(has);
+            if (rank >= c) {
+                rank -= c;
+                continue;
+            }
+            for (; rank > 0; --rank) has &= has - 1;
+            b = b0 + __ffs(has) - 1;
+            break;
+        }
+        bool bad = false;
+        seq_bounds(p.cu_q, p.total_q, b, w.q0, w.nq, bad);
+        seq_bounds(p.cu_k, p.total_k, b, w.k0, w.nk, bad);
+        w.tok = lo * item_tokens(p);
+        w.hk = item % p.kv_heads;
+        w.part = -1;
+        fill_work(p, w, 0, INT_MAX);
+        return w;
+    }
+};
+
+// The list of all key blocks, for ranges: sequences in order; in each the tiles, in each the
+// key heads, in each the sequence's key blocks (at least one, so that every row is written).
+struct List {
+    W4_DEV static int blocks_of(int nk) { return max(1, (nk + kKeys - 1) / kKeys); }
+    // Blocks of sequence b.
+    W4_DEV static long long size(const AttnParams& p, int b) {
+        int s, nq, nk;
+        bool bad = false;
+        seq_bounds(p.cu_q, p.total_q, b, s, nq, bad);
+        seq_bounds(p.cu_k, p.total_k, b, s, nk, bad);
+        return (long long)((nq + p.tpt - 1) / p.tpt) * p.kv_heads * blocks_of(nk);
+    }
+    // Blocks of the sequences before b (b = batch: of all), by one warp.
+    W4_DEV static long long before(const AttnParams& p, int b, int lane) {
+        long long n = 0;
+        for (int c = lane; c < b; c += 32) n += size(p, c);
+#pragma unroll
+        for (int d = 16; d; d >>= 1) n += __shfl_xor_sync(0xffffffffu, n, d);
+        return n;
+    }
+    // First block of CTA c's range, and the CTA of a block.
+    W4_DEV static long long begin(const AttnParams& p, long long total, int c) {
+        return total / p.ctas * c + min((long long)c, total % p.ctas);
+    }
+    W4_DEV static int cta_of(const AttnParams& p, long long total, long long u) {
+        const long long base = total / p.ctas, rem = total % p.ctas;
+        return u < rem * (base + 1) ? (int)(u / (base + 1)) : (int)(rem + (u - rem * (base + 1)) / max(1ll, base));
+    }
+};
+
+// The items of a CTA's range, one after the other, by one warp.
+struct Walker {
+    long long at, end;    // next block of the list, end of the range
+    long long first;      // list index of sequence b's first block
+    int b;
+    W4_DEV void start(const AttnParams& p, int lane) {
+        const long long total = List::before(p, p.batch, lane);
+        at = List::begin(p, total, blockIdx.x);
+        end = List::begin(p, total, blockIdx.x + 1);
+        first = 0;
+        b = 0;
+    }
+    W4_DEV Work next(const AttnParams& p) {
+        Work w = {};
+        if (at >= end) return w;
+        long long n = List::size(p, b);
+        while (at >= first + n) {   // (at < total, so some sequence holds it)
+            first += n;
+            n = List::size(p, ++b);
+        }
+        bool bad = false;
+        seq_bounds(p.cu_q, p.total_q, b, w.q0, w.nq, bad);
+        seq_bounds(p.cu_k, p.total_k, b, w.k0, w.nk, bad);
+        const int nb = List::blocks_of(w.nk);
+        const int run = (int)((at - first) / nb), from = (int)((at - first) % nb);
+        const int to = (int)min((long long)nb, from + (end - at));
+        w.tok = run / p.kv_heads * p.tpt;
+        w.hk = run % p.kv_heads;
+        // a part that starts inside its item is the CTA's first, one that starts the item and
+        // does not end it the last: two places a CTA
+        w.part = from == 0 && to == nb ? -1 : 2 * (int)blockIdx.x + (from == 0 ? 1 : 0);
+        fill_work(p, w, from, to);
+        at += to - from;
+        return w;
+    }
+};
 
 // The row of this softmax thread.
 struct Row {
     int tok, head, limit;   // token in the sequence, query head, keys the row sees
     bool live;              // the row is a token of the sequence
 };
-W4_DEV Row row_of(const AttnParams& p, const Work& w, int x) {
+W4_DEV Row row_of(const AttnParams& p, const volatile Work* w, int x) {
     const int row = threadIdx.x & (kRows - 1);
     Row r;
-    r.tok = w.tok + x * p.tpt + row / p.group;
-    r.head = w.hk * p.group + row % p.group;
-    r.live = w.valid && row < p.tpt * p.group && r.tok < w.nq;
-    r.limit = !r.live ? 0 : p.causal ? max(0, min(w.nk, r.tok + 1 + w.nk - w.nq)) : w.nk;
+    r.tok = w->tok + (p.tiles == 2 ? x * p.tpt : 0) + row / p.group;
+    r.head = w->hk * p.group + row % p.group;
+    r.live = row < p.tpt * p.group && r.tok < w->nq;
+    r.limit = !r.live ? 0 : p.causal ? max(0, min(w->nk, r.tok + 1 + w->nk - w->nq)) : w->nk;
     return r;
 }
-W4_DEV Work reload(const volatile Work* s) {
-    Work w;
-    w.valid = s->valid;
-    w.q0 = s->q0;
-    w.nq = s->nq;
-    w.k0 = s->k0;
-    w.nk = s->nk;
-    w.tok = s->tok;
-    w.hk = s->hk;
-    return w;
+
+// ---------------------------------------------------------------- next item
+// Ask for a CTA that has not started yet, in whose place this one carries on; the answer
+// (16 bytes) completes on the barrier.
+W4_DEV void ask_next(void* answer, uint64_t* bar) {
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+            smem_u32(answer)),
+        "r"(smem_u32(bar))
+        : "memory");
+}
+// Its block index, or -1 when every CTA has started.
+W4_DEV int answered(const void* answer) {
+    uint32_t x = 0, ok = 0;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 h;\n\tld.shared.b128 h, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+        "selp.u32 %1, 1, 0, p;\n\tmov.u32 %0, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, _, _, _}, h;\n\t}"
+        : "=r"(x), "=r"(ok)
+        : "r"(smem_u32(answer))
+        : "memory");
+    return ok ? (int)x : -1;
 }
 
 // ---------------------------------------------------------------- tensor memory
@@ -276,15 +411,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* empty = full + S;
     uint64_t* raw = empty + S;       // a V tile of a masked block has landed,
     uint64_t* fixed = raw + S;       // ... and is finite (these tiles do not signal `full`)
-    uint64_t* q_full = fixed + S;
-    uint64_t* s_full = q_full + 1;      // [2]
+    uint64_t* item_full = fixed + S;          // [kItems]
+    uint64_t* item_empty = item_full + kItems;
+    uint64_t* q_full = item_empty + kItems;
+    uint64_t* q_empty = q_full + 1;
+    uint64_t* s_full = q_empty + 1;     // [2]
     uint64_t* p_full = s_full + 2;      // [2]
     uint64_t* o_done = p_full + 2;      // [2]
-    uint64_t* all_done = o_done + 2;
+    uint64_t* next_bar = o_done + 2;
+    uint64_t* all_done = next_bar + 1;
+    uint64_t* both_ready = all_done + 1;   // one tile: A's and B's O and statistics are there,
+    uint64_t* both_read = both_ready + 1;  // ... and have been read
+    float2* stats = reinterpret_cast<float2*>(smem + C::stats);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::misc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::misc + 4);
-    volatile int* poison = reinterpret_cast<volatile int*>(smem + C::misc + 8);
-    Work* s_work = reinterpret_cast<Work*>(smem + C::misc + 16);
+    auto slot = [&](int i) { return reinterpret_cast<Work*>(smem + C::items + (i % kItems) * 64); };
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -292,17 +433,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
             mbar_init(&raw[s], 1);
-            mbar_init(&fixed[s], 64);
+            mbar_init(&fixed[s], 2);
+        }
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(&item_full[i], 1);
+            mbar_init(&item_empty[i], 8 + 1 + 2);
         }
         mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
         for (int x = 0; x < 2; ++x) {
             mbar_init(&s_full[x], 1);
-            mbar_init(&p_full[x], 128);
+            mbar_init(&p_full[x], 4);
             mbar_init(&o_done[x], 1);
         }
+        mbar_init(next_bar, 1);
         mbar_init(all_done, 1);
+        mbar_init(both_ready, 8);
+        mbar_init(both_read, 8);
         *abort_flag = 0;
-        *poison = 0;
         fence_mbar_init();
     }
     if (warp == 9) {
@@ -314,70 +462,117 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tensormap(&tmap_k);
         prefetch_tensormap(&tmap_v);
     }
-    pdl_launch_dependents();
-    pdl_wait();   // everything read below may come from the preceding kernel
-    if (warp == 0) {
-        const Work w = find_work(p, blockIdx.x / p.kv_heads, blockIdx.x % p.kv_heads, lane);
-        if (lane == 0) *s_work = w;
-        if (blockIdx.x == 0) {
-            bool bad = false;
-            for (int b = lane; b < p.batch; b += 32) {
-                int s, n;
-                seq_bounds(p.cu_q, p.total_q, b, s, n, bad);
-                seq_bounds(p.cu_k, p.total_k, b, s, n, bad);
-            }
-            if (bad) atomicOr(&g_w4_error_word, W4_DEVERR_GIDX);
-        }
-    }
     w4p::tc_fence_before();
     __syncthreads();
     w4p::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const Work w = *s_work;
-    const int nkeys[2] = {tile_keys(p, w, 0), tile_keys(p, w, 1)};
-    const int nb0 = w.valid ? (nkeys[0] + kKeys - 1) / kKeys : 0;
-    const int nb1 = w.valid ? (nkeys[1] + kKeys - 1) / kKeys : 0;
-    const int nb = max(nb0, nb1);
-    // blocks from mfirst on hold a key that some row of the pair does not see
-    const int mfirst = common_keys(p, w) / kKeys;
+    pdl_launch_dependents();
+    auto all = [&](bool ok) { return __all_sync(0xffffffffu, ok) != 0; };
+    // the item in slot n % kItems, for consumer warps; false at the end
+    auto take = [&](int n, bool& ok) {
+        ok = all(wait_or_abort(&item_full[n % kItems], (n / kItems) & 1, abort_flag));
+        return ok && slot(n)->valid != 0;
+    };
+    auto release = [&](int n) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&item_empty[n % kItems]);
+    };
 
     if (warp >= 8) {
         w4p::setmaxnreg_dec<kRegsOther>();
         if (warp == 8) {
-            // ---------------------------------------------------------- TMA producer
-            if (lane == 0 && nb > 0) {
-                const int nq = (nb0 > 0 ? 1 : 0) + (nb1 > 0 ? 1 : 0);
-                mbar_arrive_expect_tx(q_full, nq * NC * 128 * p.group * p.tpt);
-                for (int x = 0; x < 2; ++x) {
-                    if ((x ? nb1 : nb0) == 0) continue;
-                    for (int c = 0; c < NC; ++c)
-                        tma_load_3d(smem + C::q + x * C::q_tile + c * kRows * 128, &tmap_q, 64 * c, w.hk * p.group,
-                                    w.q0 + w.tok + x * p.tpt, q_full);
+            // ---------------------------------------------------------- items, TMA
+            pdl_wait();   // everything read below may come from the preceding kernel
+            if (blockIdx.x == 0) {
+                bool bad = false;
+                for (int b = lane; b < p.batch; b += 32) {
+                    int s, n;
+                    seq_bounds(p.cu_q, p.total_q, b, s, n, bad);
+                    seq_bounds(p.cu_k, p.total_k, b, s, n, bad);
                 }
-                // ring order: K_0, V_0, K_1, V_1, ...  Each barrier completes once a use, so
-                // its parity is a bit that its users flip at each use.
-                uint32_t full_ph = 0, raw_ph = 0, last_raw = 0;   // a bit a stage
-                int i = 0;
-                for (; i < 2 * nb; ++i) {
-                    const int s = i % S;
-                    if (i >= S && !wait_or_abort(&empty[s], ((i / S) & 1) ^ 1, abort_flag)) break;
-                    const bool is_raw = (i & 1) && i / 2 >= mfirst;
-                    uint64_t* bar = is_raw ? &raw[s] : &full[s];
-                    if (is_raw) raw_ph ^= 1u << s;
-                    else full_ph ^= 1u << s;
-                    last_raw = (last_raw & ~(1u << s)) | ((is_raw ? 1u : 0u) << s);
-                    mbar_arrive_expect_tx(bar, C::kv_tile);
-                    for (int c = 0; c < NC; ++c)
-                        tma_load_3d(smem + C::ring + s * C::kv_tile + c * kKeys * 128, (i & 1) ? &tmap_v : &tmap_k, 64 * c,
-                                    w.hk, w.k0 + (i / 2) * kKeys, bar);
-                }
-                if (*abort_flag) {
-                    // the copies in flight land before the block ends
-                    (void)mbar_wait(q_full, 0);
-                    for (int s = 0; s < min(S, i); ++s) {
-                        const bool r = (last_raw >> s) & 1u;
-                        (void)mbar_wait(r ? &raw[s] : &full[s], (((r ? raw_ph : full_ph) >> s) & 1u) ^ 1u);
+                if (bad) atomicOr(&g_w4_error_word, W4_DEVERR_GIDX);
+            }
+            const bool ranges = p.part_o != nullptr;
+            Finder finder = {};
+            Walker walker = {};
+            if (ranges) walker.start(p, lane);
+            else finder.start(p, lane);
+            int item = blockIdx.x;
+            int i = 0, nq = 0;   // ring position, Q loads so far
+            // Each barrier completes once a use, so its parity is a bit that its users flip
+            // at each use (a bit a stage).
+            uint32_t full_ph = 0, raw_ph = 0, last_raw = 0;
+            bool ok = true, asked = false;
+            int n = 0;
+            for (; ok; ++n) {
+                const Work w = ranges ? walker.next(p) : finder.find(p, item, lane);
+                if (n >= kItems) ok = all(wait_or_abort(&item_empty[n % kItems], ((n / kItems) & 1) ^ 1, abort_flag));
+                if (!ok) break;
+                const bool more = w.valid && !ranges;
+                if (lane == 0) {
+                    *slot(n) = w;
+                    mbar_arrive(&item_full[n % kItems]);
+                    if (more) {
+                        mbar_arrive_expect_tx(next_bar, 16);
+                        ask_next(smem + C::next, next_bar);
                     }
+                }
+                if (!w.valid) break;
+                asked = more;
+                const bool pair = p.tiles == 2;
+                const int nb = pair ? max(w.nb0, w.nb1) : w.nb0 + w.nb1;
+                if (lane == 0 && nb > 0) {
+                    // Q, then through the ring, in the order the products take them: K_0, V_0, K_1,
+                    // V_1, ... (pair) or K_0, K_1, V_0, K_2, V_1, K_3, ... (one tile)
+                    if (nq > 0) ok = wait_or_abort(q_empty, (nq - 1) & 1, abort_flag);
+                    if (ok) {
+                        const int tiles = pair ? (w.nb0 > 0 ? 1 : 0) + (w.nb1 > 0 ? 1 : 0) : 1;
+                        mbar_arrive_expect_tx(q_full, tiles * NC * 128 * p.group * p.tpt);
+                        ++nq;
+                        for (int x = 0; x < p.tiles; ++x) {
+                            if ((x ? w.nb1 : w.nb0) == 0) continue;
+                            for (int c = 0; c < NC; ++c)
+                                tma_load_3d(smem + C::q + x * C::q_tile + c * kRows * 128, &tmap_q, 64 * c,
+                                            w.hk * p.group, w.q0 + w.tok + x * p.tpt, q_full);
+                        }
+                    }
+                    const int lead = pair ? 1 : min(2, nb);   // K tiles ahead of the first V
+                    for (int k = 0, nk = 0, nv = 0; k < 2 * nb && ok; ++k, ++i) {
+                        const int s = i % S;
+                        const bool is_v = nk == nb || nk - nv == lead;
+                        const int blk = is_v ? nv++ : nk++;
+                        if (i >= S) ok = wait_or_abort(&empty[s], ((i / S) & 1) ^ 1, abort_flag);
+                        if (!ok) break;
+                        const bool is_raw = is_v && blk >= w.mfirst;
+                        uint64_t* bar = is_raw ? &raw[s] : &full[s];
+                        if (is_raw) raw_ph ^= 1u << s;
+                        else full_ph ^= 1u << s;
+                        last_raw = (last_raw & ~(1u << s)) | ((is_raw ? 1u : 0u) << s);
+                        mbar_arrive_expect_tx(bar, C::kv_tile);
+                        for (int c = 0; c < NC; ++c)
+                            tma_load_3d(smem + C::ring + s * C::kv_tile + c * kKeys * 128, is_v ? &tmap_v : &tmap_k,
+                                        64 * c, w.hk, w.k0 + (w.b0 + blk) * kKeys, bar);
+                    }
+                }
+                ok = all(ok);
+                if (ranges) continue;
+                if (!all(mbar_wait(next_bar, n & 1))) {
+                    *abort_flag = 1;
+                    break;
+                }
+                asked = false;
+                item = answered(smem + C::next);
+                fence_proxy_async_smem();   // the answer is read before it is written again
+                __syncwarp();
+                if (item < 0) item = INT_MAX;   // found as the end
+            }
+            if (*abort_flag && lane == 0) {
+                // what is in flight lands before the block ends
+                if (asked) (void)mbar_wait(next_bar, n & 1);
+                if (nq > 0) (void)mbar_wait(q_full, (nq - 1) & 1);
+                for (int s = 0; s < min(S, i); ++s) {
+                    const bool r = (last_raw >> s) & 1u;
+                    (void)mbar_wait(r ? &raw[s] : &full[s], (((r ? raw_ph : full_ph) >> s) & 1u) ^ 1u);
                 }
             }
             __syncwarp();
@@ -394,13 +589,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto wait_bit = [&](uint64_t* bars, uint32_t& ph, int s) {
                 const bool r = wait_or_abort(&bars[s], (ph >> s) & 1u, abort_flag);
                 ph ^= 1u << s;
-                return __all_sync(0xffffffffu, r) != 0;
+                return all(r);
             };
-            auto all = [&](bool ok) { return __all_sync(0xffffffffu, ok) != 0; };
-            // S_x = Q_x K^T with the K tile of ring position i
-            auto issue_s = [&](int x, int i) {
+            // S_x = Q_q K^T with the K tile of ring position i
+            auto issue_s = [&](int x, int q, int i) {
                 if (!leader) return;
-                const uint32_t qd = qd0 + ((x * C::q_tile) >> 4);
+                const uint32_t qd = qd0 + ((q * C::q_tile) >> 4);
                 const uint32_t kd = kd0 + (((i % S) * C::kv_tile) >> 4);
 #pragma unroll
                 for (int c = 0; c < NC; ++c)
@@ -410,46 +604,105 @@ __global__ void __launch_bounds__(kThreads, 1)
                                   kd + ((c * kKeys * 128 + 32 * k) >> 4), hi, idesc_s, (c | k) ? 1u : 0u);
                 w4p::tc_commit(&s_full[x]);
             };
-            bool ok = nb > 0;
-            if (ok) {
-                ok = all(wait_or_abort(q_full, 0, abort_flag)) && wait_bit(full, full_ph, 0);
-                w4p::tc_fence_after();
-                if (ok) {
-                    if (nb0 > 0) issue_s(0, 0);
-                    if (nb1 > 0) issue_s(1, 0);
-                    if (leader) w4p::tc_commit(&empty[0]);
-                }
-            }
-            for (int j = 0; j < nb && ok; ++j) {
-                const int iv = 2 * j + 1, ik = 2 * j + 2;   // ring positions of V_j and K_{j+1}
-                const int sv = iv % S;
-                ok = j >= mfirst ? wait_bit(fixed, fixed_ph, sv) : wait_bit(full, full_ph, sv);
-                if (!ok) break;
-                if (j + 1 < nb) ok = wait_bit(full, full_ph, ik % S);
-                if (!ok) break;
+            // O_x (+)= P_x V with the V tile of ring position i
+            auto issue_o = [&](int x, int i, bool first) {
+                if (!leader) return;
+                const uint32_t vd = vd0 + (((i % S) * C::kv_tile) >> 4);
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const int n = x ? nb1 : nb0;
-                    if (j < n) {
-                        ok = ok && all(wait_or_abort(&p_full[x], j & 1, abort_flag));
+                for (int k = 0; k < kKeys / 16; ++k)
+                    tc_mma_ts(tmem + 256 + DP * x, tmem + 128 * x + 8 * k, vd + ((2048 * k) >> 4), hi, idesc_o,
+                              (first && k == 0) ? 0u : 1u);
+                w4p::tc_commit(&o_done[x]);
+            };
+            int pos = 0, nq = 0;       // ring position, Q loads so far
+            uint32_t p_ph = 0;         // parity of the next P tile of A (bit 0), of B (bit 1)
+            bool ok = true;
+            auto wait_p = [&](int x) {
+                const bool r = wait_or_abort(&p_full[x], (p_ph >> x) & 1u, abort_flag);
+                p_ph ^= 1u << x;
+                return all(r);
+            };
+            auto free_slot = [&](int i) {
+                if (leader) w4p::tc_commit(&empty[i % S]);
+            };
+            for (int n = 0; ok && take(n, ok); ++n) {
+                const Work* w = slot(n);
+                const int nb0 = w->nb0, nb1 = w->nb1, mfirst = w->mfirst;
+                if (nb0 + nb1 == 0) {
+                    release(n);
+                    continue;
+                }
+                ok = all(wait_or_abort(q_full, nq & 1, abort_flag));
+                ++nq;
+                if (p.tiles == 2) {
+                    // both tiles over the same blocks: K_0, then V_j and K_{j+1}
+                    const int nb = max(nb0, nb1);
+                    ok = ok && wait_bit(full, full_ph, pos % S);
+                    if (!ok) break;
+                    w4p::tc_fence_after();
+                    if (nb0 > 0) issue_s(0, 0, pos);
+                    if (nb1 > 0) issue_s(1, 1, pos);
+                    free_slot(pos);
+                    if (leader && nb == 1) w4p::tc_commit(q_empty);
+                    ++pos;
+                    for (int j = 0; j < nb; ++j) {
+                        const int iv = pos, ik = pos + 1;
+                        ok = j >= mfirst ? wait_bit(fixed, fixed_ph, iv % S) : wait_bit(full, full_ph, iv % S);
+                        if (ok && j + 1 < nb) ok = wait_bit(full, full_ph, ik % S);
+                        if (!ok) break;
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const int nx = x ? nb1 : nb0;
+                            if (j < nx) {
+                                ok = ok && wait_p(x);
+                                if (!ok) break;
+                                w4p::tc_fence_after();
+                                issue_o(x, iv, j == 0);
+                            }
+                            if (j + 1 < nx) issue_s(x, x, ik);
+                        }
+                        if (!ok) break;
+                        free_slot(iv);
+                        ++pos;
+                        if (j + 1 < nb) {
+                            free_slot(ik);
+                            ++pos;
+                        }
+                        if (leader && j + 2 == nb) w4p::tc_commit(q_empty);   // the item's last S is issued
+                    }
+                } else {
+                    // one tile: A takes the even blocks, B the odd ones
+                    const int nb = nb0 + nb1;
+                    for (int x = 0; x < min(2, nb) && ok; ++x) {
+                        ok = wait_bit(full, full_ph, pos % S);
                         if (!ok) break;
                         w4p::tc_fence_after();
-                        if (leader) {
-                            const uint32_t vd = vd0 + ((sv * C::kv_tile) >> 4);
-#pragma unroll
-                            for (int k = 0; k < kKeys / 16; ++k)
-                                tc_mma_ts(tmem + 256 + DP * x, tmem + 128 * x + 8 * k, vd + ((2048 * k) >> 4), hi, idesc_o,
-                                          (j | k) ? 1u : 0u);
-                            w4p::tc_commit(&o_done[x]);
+                        issue_s(x, 0, pos);
+                        free_slot(pos);
+                        ++pos;
+                    }
+                    if (leader && nb <= 2) w4p::tc_commit(q_empty);
+                    for (int k = 0; k < nb && ok; ++k) {
+                        const int x = k & 1;
+                        ok = k >= mfirst ? wait_bit(fixed, fixed_ph, pos % S) : wait_bit(full, full_ph, pos % S);
+                        ok = ok && wait_p(x);
+                        if (!ok) break;
+                        w4p::tc_fence_after();
+                        issue_o(x, pos, k < 2);
+                        free_slot(pos);
+                        ++pos;
+                        if (k + 2 < nb) {
+                            ok = wait_bit(full, full_ph, pos % S);
+                            if (!ok) break;
+                            w4p::tc_fence_after();
+                            issue_s(x, 0, pos);
+                            free_slot(pos);
+                            ++pos;
+                            if (leader && k + 3 == nb) w4p::tc_commit(q_empty);
                         }
                     }
-                    if (j + 1 < n) issue_s(x, ik);
                 }
-                if (!ok) break;
-                if (leader) {
-                    w4p::tc_commit(&empty[sv]);
-                    if (j + 1 < nb) w4p::tc_commit(&empty[ik % S]);
-                }
+                if (ok) release(n);
             }
             if (leader) w4p::tc_commit(all_done);
             (void)mbar_wait(all_done, 0);
@@ -458,58 +711,75 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ---------------------------------------------------------- V of masked blocks
             const int t = (warp - 10) * 32 + lane;
             uint32_t raw_ph = 0;
-            for (int j = mfirst; j < nb; ++j) {
-                const int s = (2 * j + 1) % S;
-                if (!wait_or_abort(&raw[s], (raw_ph >> s) & 1u, abort_flag)) break;
-                raw_ph ^= 1u << s;
-                const int left = w.nk - j * kKeys;   // keys of the block that belong to the sequence
-                unsigned char* v = smem + C::ring + s * C::kv_tile;
-                bool any = false, wrote = false;
-                for (int q = t; q < NC * kKeys * 8; q += 64) {
-                    uint4* at = reinterpret_cast<uint4*>(v + q * 16);
-                    uint4 d = *at;
-                    if (((q >> 3) & (kKeys - 1)) >= left) {
-                        *at = make_uint4(0u, 0u, 0u, 0u);
-                        wrote = true;
-                        continue;
-                    }
-                    uint32_t e[4] = {d.x, d.y, d.z, d.w};
-                    constexpr uint32_t kExp = BF16 ? 0x7F80u : 0x7C00u;
-                    bool hit = false;
+            int base = 0;
+            bool ok = true;
+            for (int n = 0; ok && take(n, ok); ++n) {
+                Work* w = slot(n);
+                const bool pair = p.tiles == 2;
+                const int nb = pair ? max(w->nb0, w->nb1) : w->nb0 + w->nb1;
+                for (int j = w->mfirst; j < nb; ++j) {
+                    // ring position of V_j: behind the K tiles that lead it
+                    const int lead = pair ? 1 : min(2, nb);
+                    const int s = (base + j + min(j + lead, nb)) % S;
+                    ok = all(wait_or_abort(&raw[s], (raw_ph >> s) & 1u, abort_flag));
+                    if (!ok) break;
+                    raw_ph ^= 1u << s;
+                    const int left = w->nk - (w->b0 + j) * kKeys;   // keys of the block that the sequence has
+                    unsigned char* v = smem + C::ring + s * C::kv_tile;
+                    constexpr uint32_t kExp = BF16 ? 0x7F807F80u : 0x7C007C00u;
+                    constexpr uint32_t kOne = BF16 ? 0x00800080u : 0x04000400u;
+                    bool any = false;
+#pragma unroll 4
+                    for (int q = t; q < NC * kKeys * 8; q += 64) {
+                        uint4* at = reinterpret_cast<uint4*>(v + q * 16);
+                        const uint4 d = *at;
+                        uint32_t e[4] = {d.x, d.y, d.z, d.w};
+                        // an exponent of all ones carries into the sign's place
+                        uint32_t hit = 0;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        if ((e[k] & kExp) == kExp) {
-                            e[k] &= 0xFFFF0000u;
-                            hit = true;
+                        for (int k = 0; k < 4; ++k) hit |= (e[k] & kExp) + kOne;
+                        const bool behind = ((q >> 3) & (kKeys - 1)) >= left;
+                        if (!behind && !(hit & 0x80008000u)) continue;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t bad = ((e[k] & kExp) + kOne) & 0x80008000u;
+                            e[k] = behind ? 0u : e[k] & ~((bad >> 15) * 0xFFFFu);
                         }
-                        if (((e[k] >> 16) & kExp) == kExp) {
-                            e[k] &= 0x0000FFFFu;
-                            hit = true;
-                        }
-                    }
-                    if (hit) {
                         *at = make_uint4(e[0], e[1], e[2], e[3]);
-                        any = wrote = true;
+                        any |= !behind;
                     }
+                    if (any) *reinterpret_cast<volatile int*>(&w->poison) = 1;
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&fixed[s]);
                 }
-                if (any) *poison = 1;
-                if (wrote) fence_proxy_async_smem();
-                mbar_arrive(&fixed[s]);
+                base += 2 * nb;
+                release(n);
             }
         }
     } else {
         // -------------------------------------------------------------- softmax, one row a thread
         w4p::setmaxnreg_inc<kRegsSoftmax>();
+        pdl_wait();   // before any store
         const int x = warp >> 2;
-        const int n = x ? nb1 : nb0;
-        const int limit = row_of(p, w, x).limit;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t ts = tmem + lanes + 128 * x, to = tmem + lanes + 256 + DP * x;
-        float m = -INFINITY, l = 0.0f;   // reference maximum of the raw scores, sum of the weights
+        int cnt = 0, ones = 0;   // S tiles, one-tile items so far
         bool ok = true;
-        for (int j = 0; j < n; ++j) {
-            ok = __all_sync(0xffffffffu, wait_or_abort(&s_full[x], j & 1, abort_flag));
+        for (int item = 0; ok && take(item, ok); ++item) {
+        const volatile Work* const ws = slot(item);
+        float m = -INFINITY, l = 0.0f;   // reference maximum of the raw scores, sum of the weights
+        const int n = x ? ws->nb1 : ws->nb0;
+        const int mfirst = ws->mfirst;
+        const Row mine = row_of(p, ws, x);
+        const int limit = mine.limit - ws->b0 * kKeys;   // in the item's keys
+        const bool busy = __any_sync(0xffffffffu, mine.live);
+        const bool pair = p.tiles == 2;
+        for (int t = 0; t < n; ++t, ++cnt) {
+            const int j = pair ? t : 2 * t + x;   // key block
+            ok = all(wait_or_abort(&s_full[x], cnt & 1, abort_flag));
             if (!ok) break;
+            if (busy) {   // (P of rows that are no tokens may be anything)
             w4p::tc_fence_after();
             uint32_t sr[8][16];
 #pragma unroll
@@ -533,9 +803,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (__any_sync(0xffffffffu, raise)) {
                 const float nm = raise ? bm : m;
                 const float f = raise ? ex2((m - nm) * p.scale_log2) : 1.0f;
-                if (j > 0) {
-                    // O is complete up to block j - 1 (its P V must be done), then rescaled
-                    ok = __all_sync(0xffffffffu, wait_or_abort(&o_done[x], (j - 1) & 1, abort_flag));
+                if (t > 0) {
+                    // O is complete up to the last block (its P V must be done), then rescaled
+                    ok = all(wait_or_abort(&o_done[x], (cnt - 1) & 1, abort_flag));
                     if (!ok) break;
                     w4p::tc_fence_after();
 #pragma unroll
@@ -570,64 +840,133 @@ __global__ void __launch_bounds__(kThreads, 1)
             l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
             tmem_wait_st();
             w4p::tc_fence_before();
-            mbar_arrive(&p_full[x]);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[x]);
         }
-        // epilogue
-        if (n > 0 && ok) ok = __all_sync(0xffffffffu, wait_or_abort(&o_done[x], (n - 1) & 1, abort_flag));
+        // the item's output
+        if (n > 0 && ok) ok = all(wait_or_abort(&o_done[x], (cnt - 1) & 1, abort_flag));
+        if (!ok) break;
+        // weights of this warp's O and, with one tile, of the other's O of the same rows
+        float own = 1.0f, other = 0.0f;
+        if (!pair) {
+            stats[x * kRows + (threadIdx.x & (kRows - 1))] = make_float2(m, l);
+            w4p::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(both_ready);
+            ok = all(wait_or_abort(both_ready, ones & 1, abort_flag));
+            if (!ok) break;
+            const float2 o = stats[(1 - x) * kRows + (threadIdx.x & (kRows - 1))];
+            const float top = fmaxf(m, o.x);
+            own = m == -INFINITY ? 0.0f : ex2((m - top) * p.scale_log2);
+            other = o.x == -INFINITY ? 0.0f : ex2((o.x - top) * p.scale_log2);
+            l = own * l + other * o.y;
+            m = top;
+        }
         w4p::tc_fence_after();
-        if (ok) {
+        if (busy) {
             // read again: kept in registers through the loop, these would not fit
-            const Work w = reload(s_work);
-            const Row r = row_of(p, w, x);
-            const int tok = r.tok, head = r.head, limit = r.limit;
-            const bool live = r.live;
+            const Row r = row_of(p, ws, x);
             const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-            const size_t at = (size_t)(w.q0 + tok) * p.ldo + (size_t)head * p.hso;
-            unsigned short* O = reinterpret_cast<unsigned short*>(p.O);
-            const int bad = *poison;
+            own *= inv;
+            other *= inv;
+            const int n_other = pair ? 0 : x ? ws->nb0 : ws->nb1;
+            const bool bad = ws->poison != 0;
+            const int first = (ws->b0 + mfirst) * kKeys;   // keys whose V was looked through
+            const int last = min(r.limit, (ws->b0 + n + n_other) * kKeys);
+            const unsigned short* vrow = reinterpret_cast<const unsigned short*>(p.V) + (size_t)ws->k0 * p.ldv +
+                                         (size_t)ws->hk * p.hsv;
+            const bool part = ws->part >= 0;
+            // row offsets in the output, and where the rows of this warp that are tokens lie
+            const size_t tok = (size_t)(ws->q0 + r.tok);
+            const size_t prow = (size_t)ws->part * kRows + (threadIdx.x & (kRows - 1));
+            const size_t at = part ? prow * p.dim : tok * p.ldo + (size_t)r.head * p.hso;
+            const unsigned live = __ballot_sync(0xffffffffu, r.live);
+            unsigned char* st = smem + C::out + warp * 4096;
+            // 128 bytes of each row at a time (64 16-bit or 32 fp32 columns) through shared
+            // memory, 16-byte pieces swizzled by row: a warp then writes whole 128-byte lines
+            // of four rows instead of 16 bytes of 32
+            const int cols = part ? 32 : 64;
+#pragma unroll 1
+            for (int c0 = 0; c0 < p.dim; c0 += cols) {
+                if (!pair && (c0 / cols & 1) != x) continue;   // one tile: the two warps of a row take turns
+#pragma unroll 1
+                for (int h = 0; h < cols; h += 16) {
+                    uint32_t o[16];
+                    __syncwarp();
+                    if (n > 0) {
+                        tmem_ld16_async(to + c0 + h, o);
+                        tmem_wait_ld();
+                    }
 #pragma unroll
-            for (int c = 0; c < DP / 32; ++c) {
-                uint32_t o[32];
-                __syncwarp();
-                if (n > 0) {
-                    tmem_ld32_async(to + 32 * c, o);
-                    tmem_wait_ld();
-                } else {
+                    for (int i = 0; i < 16; ++i)
+                        o[i] = n > 0 && l != 0.0f ? __float_as_uint(__uint_as_float(o[i]) * own) : 0u;
+                    if (n_other > 0) {
+                        uint32_t o2[16];
+                        tmem_ld16_async(to + (x ? -DP : DP) + c0 + h, o2);
+                        tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = 0u;
-                }
-                if (live) {
+                        for (int i = 0; i < 16; ++i)
+                            if (l != 0.0f) o[i] = __float_as_uint(fmaf(__uint_as_float(o2[i]), other, __uint_as_float(o[i])));
+                    }
+                    if (bad) {
+                        // non-finite values that the spare warps took out of V, for the rows that see them
+                        for (int j = first; j < last; ++j) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(l == 0.0f ? 0.0f : __uint_as_float(o[i]) * inv);
-                if (bad) {
-                    // non-finite values that the spare warps took out of V, for the rows that see them
-                    for (int j = mfirst * kKeys; j < limit; ++j) {
-                        const unsigned short* v = reinterpret_cast<const unsigned short*>(p.V) +
-                                                  (size_t)(w.k0 + j) * p.ldv + (size_t)w.hk * p.hsv + 32 * c;
+                            for (int i = 0; i < 16; ++i) {
+                                if (c0 + h + i >= p.dim) break;
+                                const uint32_t b = vrow[(size_t)j * p.ldv + c0 + h + i];
+                                const float f = BF16 ? __uint_as_float(b << 16) : __half2float(__ushort_as_half((unsigned short)b));
+                                if (!isfinite(f)) o[i] = __float_as_uint(__uint_as_float(o[i]) + f);
+                            }
+                        }
+                    }
+                    if (part) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            if (32 * c + i >= p.dim) break;
-                            const uint32_t b = v[i];
-                            const float f = BF16 ? __uint_as_float(b << 16) : __half2float(__ushort_as_half((unsigned short)b));
-                            if (!isfinite(f)) o[i] = __float_as_uint(__uint_as_float(o[i]) + f);
+                        for (int q = 0; q < 4; ++q)
+                            *reinterpret_cast<uint4*>(st + lane * 128 + (((h / 4 + q) ^ (lane & 7)) << 4)) =
+                                make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            uint32_t e[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                e[k] = pack2<BF16>(__uint_as_float(o[8 * q + 2 * k]), __uint_as_float(o[8 * q + 2 * k + 1]));
+                            *reinterpret_cast<uint4*>(st + lane * 128 + (((h / 8 + q) ^ (lane & 7)) << 4)) =
+                                make_uint4(e[0], e[1], e[2], e[3]);
                         }
                     }
                 }
+                __syncwarp();
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (32 * c + 8 * i >= p.dim) break;
-                    uint32_t e[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        e[k] = pack2<BF16>(__uint_as_float(o[8 * i + 2 * k]), __uint_as_float(o[8 * i + 2 * k + 1]));
-                    *reinterpret_cast<uint4*>(O + at + 32 * c + 8 * i) = make_uint4(e[0], e[1], e[2], e[3]);
+                for (int k = 0; k < 8; ++k) {
+                    const int row = 4 * k + (lane >> 3), q = lane & 7;
+                    const size_t to_row = __shfl_sync(0xffffffffu, (unsigned long long)at, row);
+                    const uint4 d = *reinterpret_cast<const uint4*>(st + row * 128 + ((q ^ (row & 7)) << 4));
+                    const int col = c0 + (part ? 4 : 8) * q;
+                    if (!((live >> row) & 1u) || col >= p.dim) continue;
+                    if (part) *reinterpret_cast<uint4*>(p.part_o + to_row + col) = d;
+                    else *reinterpret_cast<uint4*>(reinterpret_cast<unsigned short*>(p.O) + to_row + col) = d;
                 }
-                }
+                __syncwarp();
             }
-            if (live && p.lse) {
-                const float v = l == 0.0f ? -INFINITY : m * p.scale + (logf(l) - kShift * 0.69314718055994531f);
-                p.lse[(size_t)(w.q0 + tok) * p.heads + head] = v;
+            const float v = l == 0.0f ? -INFINITY : m * p.scale + (logf(l) - kShift * 0.69314718055994531f);
+            if (r.live && (pair || x == 0)) {
+                if (part) p.part_lse[prow] = v;
+                else if (p.lse) p.lse[tok * p.heads + r.head] = v;
             }
+        }
+        if (!pair) {
+            // neither half writes its O or its statistics again before the other has read them
+            w4p::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(both_read);
+            ok = all(wait_or_abort(both_read, ones & 1, abort_flag));
+            w4p::tc_fence_after();
+            ++ones;
+        }
+        release(item);
         }
     }
     w4p::tc_fence_before();
@@ -636,6 +975,70 @@ __global__ void __launch_bounds__(kThreads, 1)
         w4p::tc_fence_after();
         w4p::tmem_dealloc(tmem, 512);
     }
+}
+
+// Joins the parts of an item that ranges cut: O = sum_s e^(lse_s - lse) O_s, lse = log sum_s
+// e^lse_s over its parts s.  A warp a (token, head), four columns a lane; rows of items that no
+// range cut are already there.
+template <bool BF16>
+__global__ void __launch_bounds__(256) combine_kernel(const AttnParams p) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const size_t row = (size_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (row >= (size_t)p.total_q * p.heads) return;
+    const int tok = (int)(row / p.heads), head = (int)(row % p.heads);
+    // the token's sequence: the last one that starts at or before it
+    int b = 0;
+    for (int hi = p.batch; p.cu_q && hi - b > 1;) {
+        const int mid = (b + hi) / 2;
+        if (__ldg(p.cu_q + mid) <= tok) b = mid;
+        else hi = mid;
+    }
+    int q0, nq, k0, nk;
+    bool bad = false;
+    seq_bounds(p.cu_q, p.total_q, b, q0, nq, bad);
+    seq_bounds(p.cu_k, p.total_k, b, k0, nk, bad);
+    if (tok < q0 || tok >= q0 + nq) return;   // behind the last sequence: left as it is
+    const int tile = (tok - q0) / p.tpt, hk = head / p.group, nb = List::blocks_of(nk);
+    const long long total = List::before(p, p.batch, lane);
+    const long long u = List::before(p, b, lane) + ((long long)tile * p.kv_heads + hk) * nb;
+    const int first = List::cta_of(p, total, u), last = List::cta_of(p, total, u + nb - 1);
+    if (first == last) return;
+    // part of CTA c: its last (place 1) where it starts the item, its first (place 0) otherwise
+    const int in_tile = (tok - q0 - tile * p.tpt) * p.group + head % p.group;
+    auto place = [&](int c) {
+        return (size_t)(2 * c + (c == first ? 1 : 0)) * kRows + in_tile;
+    };
+    float top = -INFINITY;
+    bool nan = false;
+    for (int c = first + lane; c <= last; c += 32) {
+        const float v = p.part_lse[place(c)];
+        top = fmaxf(top, v);
+        nan |= v != v;
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    nan = __any_sync(0xffffffffu, nan);
+    float a[4] = {0.0f, 0.0f, 0.0f, 0.0f}, sum = 0.0f;
+    const bool on = 4 * lane < p.dim;
+#pragma unroll 4
+    for (int c = first; c <= last; ++c) {
+        const float v = p.part_lse[place(c)];
+        const float f = v == -INFINITY ? 0.0f : expf(v - top);
+        sum += f;
+        const float4 o = on ? *reinterpret_cast<const float4*>(p.part_o + place(c) * p.dim + 4 * lane)
+                            : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        a[0] = fmaf(f, o.x, a[0]);
+        a[1] = fmaf(f, o.y, a[1]);
+        a[2] = fmaf(f, o.z, a[2]);
+        a[3] = fmaf(f, o.w, a[3]);
+    }
+    const float inv = nan ? NAN : sum > 0.0f ? 1.0f / sum : 0.0f;
+    if (on)
+        *reinterpret_cast<uint2*>(reinterpret_cast<unsigned short*>(p.O) + (size_t)tok * p.ldo + (size_t)head * p.hso + 4 * lane) =
+            make_uint2(pack2<BF16>(a[0] * inv, a[1] * inv), pack2<BF16>(a[2] * inv, a[3] * inv));
+    if (lane == 0 && p.lse) p.lse[row] = nan ? NAN : sum > 0.0f ? top + logf(sum) : -INFINITY;
 }
 
 }  // namespace w4t

@@ -2,6 +2,7 @@
 // validation, kernel selection by M and launches.  All device work is in the kernels of
 // w4_quant.cuh, w4_decode.cuh and w4_prefill.cuh; nothing here touches tensor data.
 #include <algorithm>
+#include <atomic>
 #include <climits>
 #include <cmath>
 #include <cstring>
@@ -54,9 +55,14 @@ int current_device() {
     return dev;
 }
 
+// (asked of the runtime once per device: every call needs it a few times)
 int sm_count(int dev) {
-    int v = 0;
+    static std::atomic<int> known[kMaxDevices];
+    if (dev < 0) return 0;
+    int v = dev < kMaxDevices ? known[dev].load(std::memory_order_relaxed) : 0;
+    if (v > 0) return v;
     if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    if (dev < kMaxDevices) known[dev].store(v, std::memory_order_relaxed);
     return v;
 }
 
@@ -1496,6 +1502,38 @@ w4_status check_attention_sizes(int32_t batch, int32_t heads, int32_t kv_heads, 
     return W4_OK;
 }
 
+// How a call is shared among the SMs.
+struct AttnPlan {
+    int tiles = 2, ctas = 0;        // tiles of an item; ranges: their number (0: items)
+    long long grid = 0;
+    size_t lse_at = 0, bytes = 0;   // workspace: partial outputs, then their lse
+};
+
+AttnPlan attention_plan(int64_t batch, int32_t heads, int32_t kv_heads, int32_t dim, int64_t q_tokens, int64_t k_tokens,
+                        int sms) {
+    AttnPlan L;
+    const int64_t tpt = w4t::kRows / (heads / kv_heads);
+    const int64_t seqs = std::max<int64_t>(1, std::min(batch, q_tokens));
+    // no sequence has more items than its share rounded up
+    auto items = [&](int64_t tiles) { return (q_tokens / (tiles * tpt) + seqs) * kv_heads; };
+    const int64_t single = items(1);
+    const int64_t blocks = (k_tokens / seqs + w4t::kKeys - 1) / w4t::kKeys;   // of an average sequence
+    const bool one_tile = q_tokens / seqs <= tpt;
+    if (single <= sms || one_tile) L.tiles = 1;
+    L.grid = items(L.tiles);
+    // Ranges for one tile a sequence over more than a few key blocks (bound by reading the
+    // keys), and for prompts of few items over many keys.
+    if (one_tile ? blocks >= 2 : (2 * single <= sms && blocks >= 4)) {
+        L.tiles = 1;
+        L.ctas = (int)std::min<int64_t>(sms, std::max<int64_t>(1, single * blocks / 2));   // two blocks each at least
+        L.grid = L.ctas;
+        auto up = [](size_t v) { return (v + 255) / 256 * 256; };
+        L.lse_at = up((size_t)2 * L.ctas * w4t::kRows * dim * 4);
+        L.bytes = L.lse_at + up((size_t)2 * L.ctas * w4t::kRows * 4);
+    }
+    return L;
+}
+
 template <bool BF16, int DP>
 w4_status launch_attention(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const w4t::AttnParams& p,
                            long long grid, int dev, cudaStream_t stream) {
@@ -1521,6 +1559,12 @@ w4_status launch_attention(const CUtensorMap& mq, const CUtensorMap& mk, const C
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, k, mq, mk, mv, p) != cudaSuccess) return W4_ERR_CUDA;
+    if (p.part_o) {
+        cfg.gridDim = dim3((unsigned)(((size_t)p.total_q * p.heads + 7) / 8));
+        cfg.blockDim = dim3(256);
+        cfg.dynamicSmemBytes = 0;
+        if (cudaLaunchKernelEx(&cfg, w4t::combine_kernel<BF16>, p) != cudaSuccess) return W4_ERR_CUDA;
+    }
     return launch_status();
 }
 
@@ -1529,7 +1573,11 @@ w4_status launch_attention(const CUtensorMap& mq, const CUtensorMap& mk, const C
 extern "C" size_t w4_prompt_attention_workspace_bytes(int32_t batch, int32_t heads, int32_t kv_heads,
                                                       int32_t head_dim, int64_t q_tokens, int64_t k_tokens) {
     if (check_attention_sizes(batch, heads, kv_heads, head_dim, q_tokens, k_tokens) != W4_OK) return 0;
-    return 0;
+    if (batch == 0 || q_tokens == 0) return 0;
+    const int dev = current_device();
+    const int sms = dev >= 0 ? sm_count(dev) : 0;
+    if (sms <= 0) return 0;
+    return attention_plan(batch, heads, kv_heads, head_dim, q_tokens, k_tokens, sms).bytes;
 }
 
 extern "C" w4_status w4_prompt_attention(const w4_attention* a, w4_dtype dtype, void* workspace,
@@ -1555,7 +1603,11 @@ extern "C" w4_status w4_prompt_attention(const w4_attention* a, w4_dtype dtype, 
         if (strides[i] >= (int64_t)1 << 38) return W4_ERR_UNSUPPORTED;   // tensor maps hold 2^40 bytes
     }
     const int dev = current_device();
-    if (dev < 0 || dev >= kMaxDevices) return W4_ERR_CUDA;
+    const int sms = dev >= 0 ? sm_count(dev) : 0;
+    if (dev >= kMaxDevices || sms <= 0) return W4_ERR_CUDA;
+    const AttnPlan L = attention_plan(a->batch, a->heads, a->kv_heads, a->head_dim, a->q_tokens, a->k_tokens, sms);
+    if (L.grid > INT_MAX) return W4_ERR_UNSUPPORTED;
+    if (L.bytes > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < L.bytes)) return W4_ERR_INVALID_ARG;
     w4t::AttnParams p;
     std::memset(&p, 0, sizeof(p));
     p.cu_q = a->cu_seqlens_q;
@@ -1575,6 +1627,12 @@ extern "C" w4_status w4_prompt_attention(const w4_attention* a, w4_dtype dtype, 
     p.total_q = (int)a->q_tokens;
     p.total_k = (int)a->k_tokens;
     p.tpt = w4t::kRows / p.group;
+    p.tiles = L.tiles;
+    p.ctas = L.ctas;
+    if (L.bytes > 0) {
+        p.part_o = reinterpret_cast<float*>(workspace);
+        p.part_lse = reinterpret_cast<float*>(reinterpret_cast<unsigned char*>(workspace) + L.lse_at);
+    }
     p.causal = a->causal;
     p.scale = a->scale;
     p.scale_log2 = a->scale * 1.44269504088896341f;
@@ -1588,16 +1646,10 @@ extern "C" w4_status w4_prompt_attention(const w4_attention* a, w4_dtype dtype, 
         !make_head_map(&mk, K, bf16, a->head_dim, a->kv_heads, kt, a->k_head_stride, a->k_token_stride, 1, w4t::kKeys) ||
         !make_head_map(&mv, V, bf16, a->head_dim, a->kv_heads, kt, a->v_head_stride, a->v_token_stride, 1, w4t::kKeys))
         return W4_ERR_CUDA;
-    // pairs of tiles: no sequence has more than its share rounded up
-    const long long pairs = a->q_tokens / (2 * p.tpt) + std::min<int64_t>(a->batch, a->q_tokens);
-    const long long grid = pairs * a->kv_heads;
-    if (grid > INT_MAX) return W4_ERR_UNSUPPORTED;
-    (void)workspace;
-    (void)workspace_bytes;
     cudaStream_t strm = as_stream(stream);
     if (a->head_dim <= 64)
-        return bf16 ? launch_attention<true, 64>(mq, mk, mv, p, grid, dev, strm)
-                    : launch_attention<false, 64>(mq, mk, mv, p, grid, dev, strm);
-    return bf16 ? launch_attention<true, 128>(mq, mk, mv, p, grid, dev, strm)
-                : launch_attention<false, 128>(mq, mk, mv, p, grid, dev, strm);
+        return bf16 ? launch_attention<true, 64>(mq, mk, mv, p, L.grid, dev, strm)
+                    : launch_attention<false, 64>(mq, mk, mv, p, L.grid, dev, strm);
+    return bf16 ? launch_attention<true, 128>(mq, mk, mv, p, L.grid, dev, strm)
+                : launch_attention<false, 128>(mq, mk, mv, p, L.grid, dev, strm);
 }

@@ -89,6 +89,18 @@ CASES = [
     ([200, 77], None, 4, 1, 8),
     ([130], None, 128, 1, 64),                # 128 heads to a key head
     ([1000], None, 4, 2, 96),
+    # one tile a sequence over several key blocks (ranges), with sequences that see nothing
+    ([1, 0, 1, 1, 1], [4000, 300, 0, 1, 129], 16, 2, 128),
+    ([1], [9000], 8, 8, 64),
+    ([3, 16, 1], [16, 5000, 2000], 8, 1, 128),
+    ([1] * 40, [7 * i for i in range(40)], 4, 1, 128),          # more than 32 sequences
+    # few tiles over many keys (ranges over causal tiles)
+    ([100], [3000], 2, 2, 128),
+    ([260, 40], [2000, 41], 3, 1, 96),
+    # more than 32 prompts, longest first; one and two tiles an item
+    ([(37 * i) % 190 for i in range(45)], None, 4, 2, 64),
+    ([300] * 34, None, 8, 2, 128),
+    ([5], [2], 1, 1, 16),
 ]
 
 
@@ -106,3 +118,210 @@ def test_against_plain(case, causal, dtype):
     O, lse = w4.w4_prompt_attention(Q, K, V, cu_q, None if same else cu_k, causal=causal, return_lse=True)
     w4.w4_check_device_error()
     check(O, lse, plain(Q, K, V, q_lens, k_lens, causal, D ** -0.5), dt, max(k_lens))
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_default_is_one_sequence(causal):
+    skip_without_gpu()
+    torch = torch_mod()
+    for n, m in ((150, 150), (7, 900)):
+        Q, K, V, _, _ = make(1, [n], [m], 4, 2, 64, torch.float16)
+        O, lse = w4.w4_prompt_attention(Q, K, V, causal=causal, scale=0.25, return_lse=True)
+        check(O, lse, plain(Q, K, V, [n], [m], causal, 0.25), torch.float16, m)
+
+
+# lengths for which a call works by items (pairs, single tiles) and by ranges
+WAYS = {"pairs": ([700, 300, 500], None, 32, 8), "tiles": ([150, 60], None, 8, 2), "ranges": ([1, 2, 1], [900, 500, 130], 8, 2)}
+
+
+def way(name, D=128, dtype="bfloat16", seed=5):
+    torch = torch_mod()
+    q, k, H, Hk = WAYS[name]
+    return (q, q if k is None else k) + make(seed, q, q if k is None else k, H, Hk, D, getattr(torch, dtype))
+
+
+def call(w, **kw):
+    q, k, Q, K, V, cu_q, cu_k = w
+    return w4.w4_prompt_attention(Q, K, V, cu_q, None if q is k else cu_k, **kw)
+
+
+@pytest.mark.parametrize("name", WAYS)
+def test_slices_and_layouts(name):
+    """Q, K and V as slices of fused rows, O head-major in a wider buffer, and without lse."""
+    skip_without_gpu()
+    torch = torch_mod()
+    w = way(name)
+    q, k, Q, K, V, cu_q, cu_k = w
+    want = call(w)
+    Tq, H, D = Q.shape
+    Tk, Hk, _ = K.shape
+    kv = torch.cat([K, V], 1)                                     # rows of K and V heads
+    Qh = Q.transpose(0, 1).contiguous().transpose(0, 1)           # head-major
+    out = torch.full((H, Tq, D + 24), 3.0, device="cuda").bfloat16()
+    O = out[:, :, 8:8 + D].transpose(0, 1)
+    got = w4.w4_prompt_attention(Qh, kv[:, :Hk], kv[:, Hk:], cu_q, None if q is k else cu_k, O=O)
+    assert got is O and torch.equal(O, want)
+    assert (out[:, :, :8] == 3).all() and (out[:, :, 8 + D:] == 3).all()
+
+
+@pytest.mark.parametrize("name", WAYS)
+def test_rows_behind_the_last_sequence_stay(name):
+    skip_without_gpu()
+    torch = torch_mod()
+    w = way(name)
+    q, k, Q, K, V, cu_q, cu_k = w
+    want = call(w)
+    pad = lambda t, v: torch.cat([t, torch.full((70,) + t.shape[1:], v, device="cuda").to(t.dtype)])  # noqa: E731
+    O = pad(torch.zeros_like(Q), 9.0)
+    w4.w4_prompt_attention(pad(Q, float("nan")), pad(K, float("nan")), pad(V, float("inf")), cu_q, None if q is k else cu_k, O=O)
+    assert (O[-70:] == 9).all()
+    u = torch.finfo(torch.bfloat16).eps
+    assert torch.allclose(O[:-70].float(), want.float(), rtol=u, atol=u * 0.05)   # (the padding may change the way of working)
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("name", WAYS)
+def test_non_finite_values_reach_only_the_rows_that_see_them(name, dtype):
+    """Infinite and NaN keys and values at positions that later rows see: earlier rows and
+    other sequences are untouched, rows that see them become what IEEE arithmetic gives."""
+    skip_without_gpu()
+    torch = torch_mod()
+    w = way(name, dtype=dtype)
+    q, k, Q, K, V, cu_q, cu_k = w
+    clean, lse0 = call(w, return_lse=True)
+    for kind in ("v inf", "v nan", "k nan"):
+        V2, K2 = V.clone(), K.clone()
+        hits = []
+        for b in range(len(q)):
+            at = k[b] - 1 - (b % 2)      # the last or last but one key of each sequence
+            pos = int(cu_k[b]) + at
+            if kind == "v inf":
+                V2[pos, 0, 3] = float("inf")
+            elif kind == "v nan":
+                V2[pos, 0, 3] = float("nan")
+            else:
+                K2[pos, 0, 7] = float("nan")
+            first = max(0, q[b] - 1 - (b % 2))   # first query that sees it
+            hits.append((int(cu_q[b]) + first, int(cu_q[b + 1])))
+        O, lse = w4.w4_prompt_attention(Q, K2, V2, cu_q, None if q is k else cu_k, return_lse=True)
+        G = Q.shape[1] // K.shape[1]
+        want = clean.float()
+        for a, e in hits:
+            if kind == "k nan":
+                want[a:e, :G] = float("nan")
+            else:
+                want[a:e, :G, 3] = float("inf") if kind == "v inf" else float("nan")
+        assert torch.equal(torch.isnan(O.float()), torch.isnan(want)) and torch.equal(torch.isinf(O), torch.isinf(want)), kind
+        ok = want.isfinite()
+        assert torch.equal(O.float()[ok], want[ok]), kind
+        if kind != "k nan":
+            assert torch.equal(lse, lse0)
+
+
+@pytest.mark.parametrize("name", WAYS)
+@pytest.mark.parametrize("spread", [30.0, 0.01])
+def test_large_and_small_scores(name, spread):
+    """Scores of hundreds (one key takes all; the running maximum rises again and again) and
+    scores that hardly differ."""
+    skip_without_gpu()
+    torch = torch_mod()
+    q, k, H, Hk = WAYS[name]
+    k = q if k is None else k
+    Q, K, V, cu_q, cu_k = make(11, q, k, H, Hk, 64, torch.float16)
+    Q = (Q * spread).half()
+    # rising scores: later keys point ever more along the queries' mean
+    K = (K + 0.01 * torch.arange(K.shape[0], device="cuda")[:, None, None] * Q.float().mean(0, keepdim=True)[:, :Hk]).half()
+    O, lse = w4.w4_prompt_attention(Q, K, V, cu_q, None if q is k else cu_k, return_lse=True)
+    check(O, lse, plain(Q, K, V, q, k, True, 0.125), torch.float16, max(k))
+
+
+@pytest.mark.parametrize("name", WAYS)
+def test_captured_and_on_another_stream(name):
+    skip_without_gpu()
+    torch = torch_mod()
+    w = way(name)
+    want, lse = call(w, return_lse=True)
+    O = torch.zeros_like(want)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    call(w, O=O, stream=s)
+    s.synchronize()
+    assert torch.equal(O, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(w, O=O)
+    for _ in range(2):
+        O.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(O, want)
+    # two calls at once on two streams
+    s2 = torch.cuda.Stream()
+    O2 = torch.zeros_like(want)
+    s.wait_stream(torch.cuda.current_stream())
+    s2.wait_stream(torch.cuda.current_stream())
+    for _ in range(4):
+        call(w, O=O, stream=s)
+        call(w, O=O2, stream=s2)
+    torch.cuda.synchronize()
+    assert torch.equal(O, want) and torch.equal(O2, want)
+    w4.w4_check_device_error()
+
+
+def test_lengths_may_change_between_replays():
+    """The bounds are read on the GPU: a captured call serves other lengths of the same totals."""
+    skip_without_gpu()
+    torch = torch_mod()
+    Q, K, V, cu_q, cu_k = make(3, [100, 200, 30], [100, 200, 30], 4, 2, 64, torch.float16)
+    O = torch.zeros_like(Q)
+    graph = torch.cuda.CUDAGraph()
+    w4.w4_prompt_attention(Q, K, V, cu_q, O=O)
+    with torch.cuda.graph(graph):
+        w4.w4_prompt_attention(Q, K, V, cu_q, O=O)
+    cu_q.copy_(torch.tensor([0, 7, 290, 330], device="cuda").int())
+    graph.replay()
+    torch.cuda.synchronize()
+    lens = [7, 283, 40]
+    ref = plain(Q, K, V, lens, lens, True, 0.125)
+    _, lse = w4.w4_prompt_attention(Q, K, V, cu_q, return_lse=True)
+    check(O, lse, ref, torch.float16, 283)
+
+
+@pytest.mark.parametrize("bounds", [[0, 50, 40, 100], [-5, 20, 60, 100], [0, 30, 99, 5000]])
+def test_bad_bounds_are_reported_and_stay_inside(bounds):
+    skip_without_gpu()
+    torch = torch_mod()
+    Q, K, V, _, _ = make(4, [100], [100], 4, 2, 64, torch.float16)
+    O = torch.zeros(164, 4, 64, device="cuda").half()
+    w4.w4_prompt_attention(Q, K, V, torch.tensor(bounds, device="cuda").int(), O=O[32:132])
+    with pytest.raises(w4.W4Error) as e:
+        w4.w4_check_device_error()
+    assert e.value.status == w4.W4_ERR_DEVICE_ARG
+    assert (O[:32] == 0).all() and (O[132:] == 0).all()
+    w4.w4_check_device_error()   # reported once
+
+
+def test_empty_calls():
+    skip_without_gpu()
+    torch = torch_mod()
+    Q = torch.randn(0, 4, 64, device="cuda").half()
+    K = torch.randn(3, 2, 64, device="cuda").half()
+    assert w4.w4_prompt_attention(Q, K, K).shape == (0, 4, 64)
+    Q = torch.randn(3, 4, 64, device="cuda").half()
+    O, lse = w4.w4_prompt_attention(Q, K[:0], K[:0], return_lse=True)
+    assert (O == 0).all() and torch.isneginf(lse).all()
+    cu = torch.zeros(1, dtype=torch.int32, device="cuda")
+    w4.w4_prompt_attention(Q, Q[:, :2], Q[:, :2], cu)    # a batch of no sequences
+    w4.w4_check_device_error()
+
+
+def test_workspace_is_checked():
+    skip_without_gpu()
+    torch = torch_mod()
+    w = way("ranges")
+    with pytest.raises(w4.W4Error):
+        call(w, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    q, k, Q, K, V, _, _ = w
+    need = w4.w4_prompt_attention_workspace_bytes(len(q), Q.shape[1], K.shape[1], 128, Q.shape[0], K.shape[0])
+    ws = torch.randint(0, 256, (need,), dtype=torch.uint8, device="cuda")   # of any content
+    assert torch.equal(call(w, workspace=ws), call(w))
