@@ -18,14 +18,22 @@
 // the next item overlap the end of this one:
 //   warps 0-3, 4-7  softmax of A, B: a thread owns one row of S (tensor memory lane), then the
 //                   item's output;
-//   warp 8          finds the items, loads Q, then K and V tiles of 128 keys through a ring;
+//   warp 8          loads Q, then K and V tiles of 128 keys through a ring;
 //   warp 9          issues tcgen05.mma: S = Q K^T (128 x 128), O += P V; the two tiles take
 //                   turns, so one tile's softmax runs beside the other's products;
-//   warps 10-11     make the V tiles of masked key blocks finite (below).
+//   warp 10         finds the items, one ahead (warp 11 only fills the warpgroup).
 // P (16-bit) replaces the first half of S in tensor memory and is the A operand of P V.
 // The running maximum used in the exponent is only raised when the row's maximum passes it
 // by 8 (in powers of two): sums grow by at most 2^8, nothing is lost in fp32, and O is
 // rescaled a few times a row instead of once a key block.
+//
+// What bounds it: a pair of 128 x 128 blocks takes 4 x 512 cycles of the tensor cores and
+// 32768 exponentials, 2048 cycles at 16 a cycle and SM; but a tile's next S waits for its P V
+// (tensor memory holds two S and two O tiles, no third S), so a block's softmax is also part
+// of the loop's latency.  Handing P on by halves takes a quarter of P V out of that latency
+// (8192 tokens, 32/8 heads: 461 -> 447 us).  Tried and slower: half-size S tiles, two a
+// tile (540 us: a 128 x 64 product costs as much as a 128 x 128 one), and an eighth, a quarter
+// or a third of the exponentials as a polynomial on the FMA units (456, 467, 472 us).
 //
 // Two ways to share the work:
 //   items    longest first, one CTA an item; a running CTA takes the place of one that has
@@ -36,9 +44,10 @@
 //            (at most two a CTA) and joined by combine_kernel.
 //
 // Masked keys: their scores are replaced (not shifted) before the maximum.  A masked key's
-// P is 0, but 0 * V is NaN for an infinite or NaN V, so in key blocks that hold a masked
-// key the spare warps zero V's rows behind the sequence's end and its other non-finite
-// values, and rows that do see such a value get it added to their output.
+// P is 0, but 0 * V is NaN for an infinite or NaN V.  So before the P V of a block that holds
+// a masked key the softmax warps, while they wait for its S, look through the V rows of the
+// keys that not every row sees: rows that no row sees become zero, other non-finite values
+// zero too, and the rows that do see such a value get it added to their output.
 #pragma once
 #include <climits>
 
@@ -48,13 +57,14 @@
 namespace w4t {
 
 constexpr int kRows = 128;      // rows of a tile (tensor memory lanes)
-constexpr int kKeys = 128;      // keys of a block
+constexpr int kKeys = 128;      // keys of a block (a K or V tile of the ring)
+constexpr int kSub = 64;        // keys of half a block: P is handed on, and masked keys left out, by halves
 constexpr int kThreads = 384;
-constexpr int kRegsSoftmax = 208, kRegsOther = 88, kLaunchRegs = 168;
+constexpr int kRegsSoftmax = 216, kRegsOther = 72, kLaunchRegs = 168;
 static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * kLaunchRegs, "register split");
 constexpr float kLazy = 8.0f;   // powers of two by which a row may pass its reference maximum
 
-constexpr int kItems = 3;       // items the producer may be ahead of the output, plus one
+constexpr int kItems = 2;       // the item at work and the next one
 
 template <int DP>
 struct Cfg {
@@ -65,9 +75,9 @@ struct Cfg {
     static constexpr int ring = 2 * q_tile;
     static constexpr int out = ring + stages * kv_tile;     // 4 KB a softmax warp
     static constexpr int bars = out + 8 * 4096;
-    // full, empty, raw, fixed (per stage); item full, empty; q full, empty; per tile: s full,
-    // p full, o done; next item; all done; both ready, read
-    static constexpr int nbars = 4 * stages + 2 * kItems + 2 + 3 * 2 + 4;
+    // full, empty, raw, fixed (per stage); item full, empty; q full, empty; of A and B: s full,
+    // p full (per half of a block), o done; next item, its wish; all done; both ready, read
+    static constexpr int nbars = 4 * stages + 2 * kItems + 2 + 2 + 4 + 2 + 5;
     static constexpr int next = (bars + nbars * 8 + 15) / 16 * 16;   // cluster launch control's answer
     static constexpr int items = next + 16;
     static constexpr int misc = items + kItems * 64;
@@ -91,6 +101,7 @@ struct AttnParams {
     int tiles;               // tiles of an item: 1 or 2
     int ctas;                // ranges: their number
     int causal;
+    int tma_out;             // a warp's 32 rows are whole tokens: O goes out by TMA
     float scale, scale_log2; // scale, scale * log2 e
 };
 
@@ -103,8 +114,9 @@ struct Work {
     int hk;          // key head
     int part;        // partial output it writes, or -1: the output itself
     int b0;          // first key block
-    int nb0, nb1;    // key blocks of A, of B (one tile: together the item's, alternately)
-    int mfirst;      // the item's blocks from this one on hold a key that some row does not see
+    int sub0, sub1;  // half blocks of A, of B (one tile: blocks alternate, only the last may be half)
+    int common;      // keys (from block b0) that every row sees
+    int seen;        // keys (from block b0) that some row sees
     int poison;      // set when a non-finite value was taken out of V
 };
 static_assert(sizeof(Work) <= 64, "item slot");
@@ -129,25 +141,53 @@ W4_DEV int item_tokens(const AttnParams& p) { return p.tiles * p.tpt; }
 
 // Fills in what tile `tok` of a sequence does over its key blocks [from, to).
 W4_DEV void fill_work(const AttnParams& p, Work& w, int from, int to) {
-    // keys that some row of a tile sees, and that every row of the item sees
+    // keys that a row sees whose token is `last`
     auto sees = [&](int last) { return p.causal ? max(0, min(w.nk, last + 1 + w.nk - w.nq)) : w.nk; };
-    auto blocks = [&](int t0) {   // of the tile that starts at token t0
-        return t0 >= w.nq ? 0 : (sees(min(t0 + p.tpt, w.nq) - 1) + kKeys - 1) / kKeys;
+    auto subs = [&](int t0) {   // of the tile that starts at token t0, in [from, to)
+        const int keys = t0 >= w.nq ? 0 : min(sees(min(t0 + p.tpt, w.nq) - 1), to * kKeys);
+        return max(0, keys - from * kKeys + kSub - 1) / kSub;
     };
-    const int n0 = max(0, min(blocks(w.tok), to) - from);
+    const int n0 = subs(w.tok);
     w.valid = 1;
     w.b0 = from;
-    w.nb0 = p.tiles == 2 ? n0 : (n0 + 1) / 2;
-    w.nb1 = p.tiles == 2 ? max(0, min(blocks(w.tok + p.tpt), to) - from) : n0 / 2;
-    w.mfirst = max(0, sees(w.tok) / kKeys - from);
+    if (p.tiles == 2) {
+        w.sub0 = n0;
+        w.sub1 = subs(w.tok + p.tpt);
+    } else {
+        const int nb = (n0 + 1) / 2, short_last = n0 & 1;
+        w.sub0 = 2 * ((nb + 1) / 2) - (nb & 1 ? short_last : 0);
+        w.sub1 = 2 * (nb / 2) - (nb & 1 ? 0 : short_last);
+    }
+    w.common = max(0, sees(w.tok) - from * kKeys);
+    w.seen = sees(min(w.tok + item_tokens(p), w.nq) - 1) - from * kKeys;
 }
+W4_DEV int blocks_of_subs(int sub) { return (sub + 1) / 2; }
+
+// 32 sequences, one a lane: read once, then handed around by shuffles.
+struct Seqs {
+    int q0, nq, k0, nk;
+    W4_DEV void load(const AttnParams& p, int b) {
+        q0 = nq = k0 = nk = 0;
+        bool bad = false;
+        if (b < p.batch) {
+            seq_bounds(p.cu_q, p.total_q, b, q0, nq, bad);
+            seq_bounds(p.cu_k, p.total_k, b, k0, nk, bad);
+        }
+    }
+    W4_DEV void give(Work& w, int src) const {
+        w.q0 = __shfl_sync(0xffffffffu, q0, src);
+        w.nq = __shfl_sync(0xffffffffu, nq, src);
+        w.k0 = __shfl_sync(0xffffffffu, k0, src);
+        w.nk = __shfl_sync(0xffffffffu, nk, src);
+    }
+};
 
 // Finds items, by one warp.  The items of all sequences are taken in descending index in
 // their sequence (with causal masks, descending cost): item `idx` is at the level v with
-// f(v) > idx >= f(v + 1), f(v) = sum_b max(0, items of b - v), found by bisection.  Up to 32
-// sequences keep their counts in the lanes.
+// f(v) > idx >= f(v + 1), f(v) = sum_b max(0, items of b - v), found by bisection.
 struct Finder {
-    int mine, top;   // items of this lane's sequence, the most of any sequence
+    Seqs seqs;       // the first 32
+    int mine, top;   // items of this lane's first sequence, the most of any sequence
     W4_DEV static int items_of(const AttnParams& p, int b) {
         int s, n;
         bool bad = false;
@@ -155,17 +195,13 @@ struct Finder {
         return (n + item_tokens(p) - 1) / item_tokens(p);
     }
     W4_DEV void start(const AttnParams& p, int lane) {
-        mine = 0;
-        int most = 0;
-        for (int b = lane; b < p.batch; b += 32) {
-            const int n = items_of(p, b);
-            if (b == lane) mine = n;
-            most = max(most, n);
-        }
+        seqs.load(p, lane);
+        int most = mine = (seqs.nq + item_tokens(p) - 1) / item_tokens(p);
+        for (int b = lane + 32; b < p.batch; b += 32) most = max(most, items_of(p, b));
         top = __reduce_max_sync(0xffffffffu, most);
     }
     W4_DEV int count(const AttnParams& p, int level, int lane) const {
-        int c = lane < p.batch ? max(0, mine - level) : 0;
+        int c = max(0, mine - level);
         for (int b = lane + 32; b < p.batch; b += 32) c += max(0, items_of(p, b) - level);
         return __reduce_add_sync(0xffffffffu, c);
     }
@@ -180,26 +216,23 @@ struct Finder {
             else hi = mid;
         }
         int rank = idx - count(p, lo + 1, lane);   // among the sequences with more than lo items
-        int b = 0;
+        Seqs at = seqs;
         for (int b0 = 0; b0 < p.batch; b0 += 32) {
-            const int n = b0 + lane < p.batch ? (b0 == 0 ? mine : items_of(p, b0 + lane)) : 0;
-            unsigned has = __ballot_sync(0xffffffffu, n > lo);
+            if (b0 > 0) at.load(p, b0 + lane);
+            unsigned has = __ballot_sync(0xffffffffu, (at.nq + item_tokens(p) - 1) / item_tokens(p) > lo);
             const int c = __popc(has);
             if (rank >= c) {
                 rank -= c;
                 continue;
             }
             for (; rank > 0; --rank) has &= has - 1;
-            b = b0 + __ffs(has) - 1;
+            at.give(w, __ffs(has) - 1);
             break;
         }
-        bool bad = false;
-        seq_bounds(p.cu_q, p.total_q, b, w.q0, w.nq, bad);
-        seq_bounds(p.cu_k, p.total_k, b, w.k0, w.nk, bad);
         w.tok = lo * item_tokens(p);
-        w.hk = item % p.kv_heads;
+        w.hk = item - idx * p.kv_heads;
         w.part = -1;
-        fill_work(p, w, 0, INT_MAX);
+        fill_work(p, w, 0, INT_MAX / kKeys);
         return w;
     }
 };
@@ -208,18 +241,10 @@ struct Finder {
 // key heads, in each the sequence's key blocks (at least one, so that every row is written).
 struct List {
     W4_DEV static int blocks_of(int nk) { return max(1, (nk + kKeys - 1) / kKeys); }
-    // Blocks of sequence b.
-    W4_DEV static long long size(const AttnParams& p, int b) {
-        int s, nq, nk;
-        bool bad = false;
-        seq_bounds(p.cu_q, p.total_q, b, s, nq, bad);
-        seq_bounds(p.cu_k, p.total_k, b, s, nk, bad);
-        return (long long)((nq + p.tpt - 1) / p.tpt) * p.kv_heads * blocks_of(nk);
+    W4_DEV static long long size(const AttnParams& p, const Seqs& s) {
+        return (long long)((s.nq + p.tpt - 1) / p.tpt) * p.kv_heads * blocks_of(s.nk);
     }
-    // Blocks of the sequences before b (b = batch: of all), by one warp.
-    W4_DEV static long long before(const AttnParams& p, int b, int lane) {
-        long long n = 0;
-        for (int c = lane; c < b; c += 32) n += size(p, c);
+    W4_DEV static long long sum(long long n) {
 #pragma unroll
         for (int d = 16; d; d >>= 1) n += __shfl_xor_sync(0xffffffffu, n, d);
         return n;
@@ -236,29 +261,46 @@ struct List {
 
 // The items of a CTA's range, one after the other, by one warp.
 struct Walker {
-    long long at, end;    // next block of the list, end of the range
-    long long first;      // list index of sequence b's first block
-    int b;
+    long long at, end;     // next block of the list, end of the range
+    long long ends;        // list index behind this lane's sequence
+    Seqs seqs;             // 32 sequences, from b0 on
+    int b0;
+    // the sequences from b on; `before`: blocks of those before them
+    W4_DEV void load(const AttnParams& p, int b, long long before, int lane) {
+        b0 = b;
+        seqs.load(p, b + lane);
+        ends = b + lane < p.batch ? List::size(p, seqs) : 0;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long up = __shfl_up_sync(0xffffffffu, ends, d);
+            if (lane >= d) ends += up;
+        }
+        ends += before;
+    }
     W4_DEV void start(const AttnParams& p, int lane) {
-        const long long total = List::before(p, p.batch, lane);
+        load(p, 0, 0, lane);
+        long long total = __shfl_sync(0xffffffffu, ends, 31);
+        for (int b = 32; b < p.batch; b += 32) {
+            Seqs s;
+            s.load(p, b + lane);
+            total += List::sum(b + lane < p.batch ? List::size(p, s) : 0);
+        }
         at = List::begin(p, total, blockIdx.x);
         end = List::begin(p, total, blockIdx.x + 1);
-        first = 0;
-        b = 0;
     }
-    W4_DEV Work next(const AttnParams& p) {
+    W4_DEV Work next(const AttnParams& p, int lane) {
         Work w = {};
         if (at >= end) return w;
-        long long n = List::size(p, b);
-        while (at >= first + n) {   // (at < total, so some sequence holds it)
-            first += n;
-            n = List::size(p, ++b);
+        long long last = __shfl_sync(0xffffffffu, ends, 31);
+        while (at >= last) {   // (at < total, so some sequence holds it)
+            load(p, b0 + 32, last, lane);
+            last = __shfl_sync(0xffffffffu, ends, 31);
         }
-        bool bad = false;
-        seq_bounds(p.cu_q, p.total_q, b, w.q0, w.nq, bad);
-        seq_bounds(p.cu_k, p.total_k, b, w.k0, w.nk, bad);
+        const int src = __popc(__ballot_sync(0xffffffffu, ends <= at));
+        seqs.give(w, src);
+        const long long first = __shfl_sync(0xffffffffu, ends - List::size(p, seqs), src);
         const int nb = List::blocks_of(w.nk);
-        const int run = (int)((at - first) / nb), from = (int)((at - first) % nb);
+        const int run = (int)((at - first) / nb), from = (int)((at - first) - (long long)run * nb);
         const int to = (int)min((long long)nb, from + (end - at));
         w.tok = run / p.kv_heads * p.tpt;
         w.hk = run % p.kv_heads;
@@ -271,20 +313,50 @@ struct Walker {
     }
 };
 
-// The row of this softmax thread.
+// The row of this softmax thread: token in its tile and head in its group (rg, rh) are the same
+// for every item.
 struct Row {
-    int tok, head, limit;   // token in the sequence, query head, keys the row sees
-    bool live;              // the row is a token of the sequence
+    int tok, limit;   // token in the sequence, keys the row sees
+    bool live;        // the row is a token of the sequence
 };
-W4_DEV Row row_of(const AttnParams& p, const volatile Work* w, int x) {
-    const int row = threadIdx.x & (kRows - 1);
+W4_DEV Row row_of(const AttnParams& p, const volatile Work* w, int x, int rg) {
     Row r;
-    r.tok = w->tok + (p.tiles == 2 ? x * p.tpt : 0) + row / p.group;
-    r.head = w->hk * p.group + row % p.group;
-    r.live = row < p.tpt * p.group && r.tok < w->nq;
-    r.limit = !r.live ? 0 : p.causal ? max(0, min(w->nk, r.tok + 1 + w->nk - w->nq)) : w->nk;
+    const int nq = w->nq, nk = w->nk;
+    r.tok = w->tok + (p.tiles == 2 ? x * p.tpt : 0) + rg;
+    r.live = rg < p.tpt && r.tok < nq;
+    r.limit = !r.live ? 0 : p.causal ? max(0, min(nk, r.tok + 1 + nk - nq)) : nk;
     return r;
 }
+
+// Add to a row's staged output (16-byte pieces swizzled by the row's lane; columns c0 ..) the
+// non-finite values of V that were taken out of the product, for the keys [first, last) that
+// the row sees.  Rare: not worth registers or instructions of the common path.
+template <bool BF16>
+__device__ __noinline__ void repair_row(unsigned char* row, int lane, bool fp32, int c0, int cols, const unsigned short* v,
+                                        long long ldv, int keys) {
+    for (int j = 0; j < keys; ++j, v += ldv)
+        for (int c = 0; c < cols; ++c) {
+            const uint32_t b = v[c0 + c];
+            const float f = BF16 ? __uint_as_float(b << 16) : __half2float(__ushort_as_half((unsigned short)b));
+            if (isfinite(f)) continue;
+            const int byte = c * (fp32 ? 4 : 2);
+            unsigned char* at = row + ((((byte >> 4) ^ lane) & 7) << 4) + (byte & 15);
+            if (fp32) *reinterpret_cast<float*>(at) += f;
+            else if (BF16) *reinterpret_cast<__nv_bfloat16*>(at) = __float2bfloat16_rn(__bfloat162float(*reinterpret_cast<__nv_bfloat16*>(at)) + f);
+            else *reinterpret_cast<__half*>(at) = __float2half_rn(__half2float(*reinterpret_cast<__half*>(at)) + f);
+        }
+}
+
+// Store 64 columns x one warp's rows from swizzled shared memory (box given by the tensor map).
+W4_DEV void tma_store_3d(const CUtensorMap* map, const void* src, int32_t c0, int32_t c1, int32_t c2) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+W4_DEV void tma_store_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+W4_DEV void tma_store_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // ---------------------------------------------------------------- next item
 // Ask for a CTA that has not started yet, in whose place this one carries on; the answer
@@ -393,12 +465,33 @@ W4_DEV float ex2(float x) {
     return y;
 }
 
+// max of three, NaN if one of them is (one instruction)
+W4_DEV float max3(float a, float b, float c) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// (x, y) = (x, y) * a + b and (s, t) += (x, y): two fp32 lanes an instruction
+W4_DEV void fma2_to(float& x, float& y, float a, float b) {
+    asm("{\n\t.reg .b64 p, q, r;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %2};\n\tmov.b64 r, {%3, %3};\n\t"
+        "fma.rn.f32x2 p, p, q, r;\n\tmov.b64 {%0, %1}, p;\n\t}"
+        : "+f"(x), "+f"(y)
+        : "f"(a), "f"(b));
+}
+W4_DEV void add2_to(float& s, float& t, float x, float y) {
+    asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\t"
+        "add.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+        : "+f"(s), "+f"(t)
+        : "f"(x), "f"(y));
+}
+
 using w4p::wait_or_abort;
 
 template <bool BF16, int DP>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
-                     const __grid_constant__ CUtensorMap tmap_v, const AttnParams p) {
+                     const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap tmap_o,
+                     const AttnParams p) {
     using C = Cfg<DP>;
     constexpr int NC = DP / 64;    // 64-column chunks of a head
     constexpr int S = C::stages;
@@ -415,13 +508,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* item_empty = item_full + kItems;
     uint64_t* q_full = item_empty + kItems;
     uint64_t* q_empty = q_full + 1;
-    uint64_t* s_full = q_empty + 1;     // [2]
-    uint64_t* p_full = s_full + 2;      // [2]
-    uint64_t* o_done = p_full + 2;      // [2]
+    uint64_t* s_full = q_empty + 1;     // [A, B]
+    uint64_t* p_full = s_full + 2;      // [A, B][half of the block]
+    uint64_t* o_done = p_full + 4;      // [A, B]: the item's O
     uint64_t* next_bar = o_done + 2;
     uint64_t* all_done = next_bar + 1;
     uint64_t* both_ready = all_done + 1;   // one tile: A's and B's O and statistics are there,
     uint64_t* both_read = both_ready + 1;  // ... and have been read
+    uint64_t* want = both_read + 1;        // the loads of the item at work near their end
     float2* stats = reinterpret_cast<float2*>(smem + C::stats);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::misc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::misc + 4);
@@ -433,23 +527,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
             mbar_init(&raw[s], 1);
-            mbar_init(&fixed[s], 2);
+            mbar_init(&fixed[s], 8);
         }
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&item_full[i], 1);
-            mbar_init(&item_empty[i], 8 + 1 + 2);
+            mbar_init(&item_empty[i], 8 + 1 + 1);
         }
         mbar_init(q_full, 1);
         mbar_init(q_empty, 1);
         for (int x = 0; x < 2; ++x) {
             mbar_init(&s_full[x], 1);
-            mbar_init(&p_full[x], 4);
+            mbar_init(&p_full[2 * x], 4);
+            mbar_init(&p_full[2 * x + 1], 4);
             mbar_init(&o_done[x], 1);
         }
         mbar_init(next_bar, 1);
         mbar_init(all_done, 1);
         mbar_init(both_ready, 8);
         mbar_init(both_read, 8);
+        mbar_init(want, 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -461,6 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tensormap(&tmap_q);
         prefetch_tensormap(&tmap_k);
         prefetch_tensormap(&tmap_v);
+        prefetch_tensormap(&tmap_o);
     }
     w4p::tc_fence_before();
     __syncthreads();
@@ -480,70 +577,91 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp >= 8) {
         w4p::setmaxnreg_dec<kRegsOther>();
-        if (warp == 8) {
-            // ---------------------------------------------------------- items, TMA
-            pdl_wait();   // everything read below may come from the preceding kernel
-            if (blockIdx.x == 0) {
-                bool bad = false;
-                for (int b = lane; b < p.batch; b += 32) {
-                    int s, n;
-                    seq_bounds(p.cu_q, p.total_q, b, s, n, bad);
-                    seq_bounds(p.cu_k, p.total_k, b, s, n, bad);
-                }
-                if (bad) atomicOr(&g_w4_error_word, W4_DEVERR_GIDX);
-            }
+        if (warp == 10) {
+            // ---------------------------------------------------------- items
+            pdl_wait();   // the bounds may come from the preceding kernel
             const bool ranges = p.part_o != nullptr;
             Finder finder = {};
             Walker walker = {};
             if (ranges) walker.start(p, lane);
             else finder.start(p, lane);
-            int item = blockIdx.x;
+            int item = blockIdx.x, n = 0;
+            bool asked = false;
+            for (;; ++n) {
+                const Work w = ranges ? walker.next(p, lane) : finder.find(p, item, lane);
+                if (n >= kItems && !all(wait_or_abort(&item_empty[n % kItems], ((n / kItems) & 1) ^ 1, abort_flag))) break;
+                if (lane == 0) {
+                    *slot(n) = w;
+                    mbar_arrive(&item_full[n % kItems]);
+                }
+                __syncwarp();
+                if (!w.valid) break;
+                if (ranges) continue;
+                // no earlier: an item that waits here is one that no idle SM can take
+                if (!all(wait_or_abort(want, n & 1, abort_flag))) break;
+                asked = true;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(next_bar, 16);
+                    ask_next(smem + C::next, next_bar);
+                }
+                if (!all(wait_or_abort(next_bar, n & 1, abort_flag))) break;
+                asked = false;
+                item = answered(smem + C::next);
+                fence_proxy_async_smem();   // the answer is read before it is written again
+                __syncwarp();
+                if (item < 0) item = INT_MAX;   // found as the end
+            }
+            if (asked) (void)mbar_wait(next_bar, n & 1);   // an answer in flight lands before the block ends
+            if (blockIdx.x == 0) {
+                bool bad = false;
+                for (int b = lane; b < p.batch; b += 32) {
+                    int s, c;
+                    seq_bounds(p.cu_q, p.total_q, b, s, c, bad);
+                    seq_bounds(p.cu_k, p.total_k, b, s, c, bad);
+                }
+                if (bad) atomicOr(&g_w4_error_word, W4_DEVERR_GIDX);
+            }
+            __syncwarp();
+        } else if (warp == 8) {
+            // ---------------------------------------------------------- TMA
+            pdl_wait();   // Q, K and V may come from the preceding kernel
             int i = 0, nq = 0;   // ring position, Q loads so far
             // Each barrier completes once a use, so its parity is a bit that its users flip
             // at each use (a bit a stage).
             uint32_t full_ph = 0, raw_ph = 0, last_raw = 0;
-            bool ok = true, asked = false;
-            int n = 0;
-            for (; ok; ++n) {
-                const Work w = ranges ? walker.next(p) : finder.find(p, item, lane);
-                if (n >= kItems) ok = all(wait_or_abort(&item_empty[n % kItems], ((n / kItems) & 1) ^ 1, abort_flag));
-                if (!ok) break;
-                const bool more = w.valid && !ranges;
-                if (lane == 0) {
-                    *slot(n) = w;
-                    mbar_arrive(&item_full[n % kItems]);
-                    if (more) {
-                        mbar_arrive_expect_tx(next_bar, 16);
-                        ask_next(smem + C::next, next_bar);
-                    }
-                }
-                if (!w.valid) break;
-                asked = more;
+            bool ok = true;
+            for (int n = 0; ok && take(n, ok); ++n) {
+                const Work* w = slot(n);
+                const int nb0 = blocks_of_subs(w->sub0), nb1 = blocks_of_subs(w->sub1), mfirst = w->common / kKeys, hk = w->hk;
+                const int key0 = w->k0 + w->b0 * kKeys, tok0 = w->q0 + w->tok;
+                release(n);
                 const bool pair = p.tiles == 2;
-                const int nb = pair ? max(w.nb0, w.nb1) : w.nb0 + w.nb1;
+                const int nb = pair ? max(nb0, nb1) : nb0 + nb1;
+                if (lane == 0 && nb == 0) mbar_arrive(want);
                 if (lane == 0 && nb > 0) {
                     // Q, then through the ring, in the order the products take them: K_0, V_0, K_1,
                     // V_1, ... (pair) or K_0, K_1, V_0, K_2, V_1, K_3, ... (one tile)
                     if (nq > 0) ok = wait_or_abort(q_empty, (nq - 1) & 1, abort_flag);
                     if (ok) {
-                        const int tiles = pair ? (w.nb0 > 0 ? 1 : 0) + (w.nb1 > 0 ? 1 : 0) : 1;
+                        const int tiles = pair ? (nb0 > 0 ? 1 : 0) + (nb1 > 0 ? 1 : 0) : 1;
                         mbar_arrive_expect_tx(q_full, tiles * NC * 128 * p.group * p.tpt);
                         ++nq;
                         for (int x = 0; x < p.tiles; ++x) {
-                            if ((x ? w.nb1 : w.nb0) == 0) continue;
+                            if ((x ? nb1 : nb0) == 0) continue;
                             for (int c = 0; c < NC; ++c)
                                 tma_load_3d(smem + C::q + x * C::q_tile + c * kRows * 128, &tmap_q, 64 * c,
-                                            w.hk * p.group, w.q0 + w.tok + x * p.tpt, q_full);
+                                            hk * p.group, tok0 + x * p.tpt, q_full);
                         }
                     }
                     const int lead = pair ? 1 : min(2, nb);   // K tiles ahead of the first V
                     for (int k = 0, nk = 0, nv = 0; k < 2 * nb && ok; ++k, ++i) {
                         const int s = i % S;
+                        if (k == max(0, 2 * nb - 6)) mbar_arrive(want);   // about three blocks before the item's end
                         const bool is_v = nk == nb || nk - nv == lead;
                         const int blk = is_v ? nv++ : nk++;
                         if (i >= S) ok = wait_or_abort(&empty[s], ((i / S) & 1) ^ 1, abort_flag);
                         if (!ok) break;
-                        const bool is_raw = is_v && blk >= w.mfirst;
+                        const bool is_raw = is_v && blk >= mfirst;
                         uint64_t* bar = is_raw ? &raw[s] : &full[s];
                         if (is_raw) raw_ph ^= 1u << s;
                         else full_ph ^= 1u << s;
@@ -551,24 +669,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mbar_arrive_expect_tx(bar, C::kv_tile);
                         for (int c = 0; c < NC; ++c)
                             tma_load_3d(smem + C::ring + s * C::kv_tile + c * kKeys * 128, is_v ? &tmap_v : &tmap_k,
-                                        64 * c, w.hk, w.k0 + (w.b0 + blk) * kKeys, bar);
+                                        64 * c, hk, key0 + blk * kKeys, bar);
                     }
                 }
                 ok = all(ok);
-                if (ranges) continue;
-                if (!all(mbar_wait(next_bar, n & 1))) {
-                    *abort_flag = 1;
-                    break;
-                }
-                asked = false;
-                item = answered(smem + C::next);
-                fence_proxy_async_smem();   // the answer is read before it is written again
-                __syncwarp();
-                if (item < 0) item = INT_MAX;   // found as the end
             }
             if (*abort_flag && lane == 0) {
                 // what is in flight lands before the block ends
-                if (asked) (void)mbar_wait(next_bar, n & 1);
                 if (nq > 0) (void)mbar_wait(q_full, (nq - 1) & 1);
                 for (int s = 0; s < min(S, i); ++s) {
                     const bool r = (last_raw >> s) & 1u;
@@ -604,22 +711,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                                   kd + ((c * kKeys * 128 + 32 * k) >> 4), hi, idesc_s, (c | k) ? 1u : 0u);
                 w4p::tc_commit(&s_full[x]);
             };
-            // O_x (+)= P_x V with the V tile of ring position i
-            auto issue_o = [&](int x, int i, bool first) {
+            // O_x (+)= P_x V over half h of the block, with the V tile of ring position i
+            auto issue_o = [&](int x, int h, int i, bool first) {
                 if (!leader) return;
-                const uint32_t vd = vd0 + (((i % S) * C::kv_tile) >> 4);
+                const uint32_t vd = vd0 + (((i % S) * C::kv_tile + h * kSub * 128) >> 4);
 #pragma unroll
-                for (int k = 0; k < kKeys / 16; ++k)
-                    tc_mma_ts(tmem + 256 + DP * x, tmem + 128 * x + 8 * k, vd + ((2048 * k) >> 4), hi, idesc_o,
+                for (int k = 0; k < kSub / 16; ++k)
+                    tc_mma_ts(tmem + 256 + DP * x, tmem + 128 * x + 32 * h + 8 * k, vd + ((2048 * k) >> 4), hi, idesc_o,
                               (first && k == 0) ? 0u : 1u);
-                w4p::tc_commit(&o_done[x]);
             };
             int pos = 0, nq = 0;       // ring position, Q loads so far
-            uint32_t p_ph = 0;         // parity of the next P tile of A (bit 0), of B (bit 1)
+            uint32_t p_ph = 0;         // parities of the next P halves, bit 2 x + h
             bool ok = true;
-            auto wait_p = [&](int x) {
-                const bool r = wait_or_abort(&p_full[x], (p_ph >> x) & 1u, abort_flag);
-                p_ph ^= 1u << x;
+            auto wait_p = [&](int x, int h) {
+                const bool r = wait_or_abort(&p_full[2 * x + h], (p_ph >> (2 * x + h)) & 1u, abort_flag);
+                p_ph ^= 1u << (2 * x + h);
                 return all(r);
             };
             auto free_slot = [&](int i) {
@@ -627,8 +733,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             for (int n = 0; ok && take(n, ok); ++n) {
                 const Work* w = slot(n);
-                const int nb0 = w->nb0, nb1 = w->nb1, mfirst = w->mfirst;
-                if (nb0 + nb1 == 0) {
+                const int sub0 = w->sub0, sub1 = w->sub1, mfirst = w->common / kKeys;
+                const int nb0 = blocks_of_subs(sub0), nb1 = blocks_of_subs(sub1);
+                if (sub0 + sub1 == 0) {
                     release(n);
                     continue;
                 }
@@ -645,21 +752,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                     free_slot(pos);
                     if (leader && nb == 1) w4p::tc_commit(q_empty);
                     ++pos;
-                    for (int j = 0; j < nb; ++j) {
+                    for (int j = 0; j < nb && ok; ++j) {
                         const int iv = pos, ik = pos + 1;
                         ok = j >= mfirst ? wait_bit(fixed, fixed_ph, iv % S) : wait_bit(full, full_ph, iv % S);
                         if (ok && j + 1 < nb) ok = wait_bit(full, full_ph, ik % S);
                         if (!ok) break;
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
-                            const int nx = x ? nb1 : nb0;
-                            if (j < nx) {
-                                ok = ok && wait_p(x);
-                                if (!ok) break;
+                            const int sub = x ? sub1 : sub0;
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                if (!ok || 2 * j + h >= sub) continue;
+                                ok = wait_p(x, h);
+                                if (!ok) continue;
                                 w4p::tc_fence_after();
-                                issue_o(x, iv, j == 0);
+                                issue_o(x, h, iv, j == 0 && h == 0);
                             }
-                            if (j + 1 < nx) issue_s(x, x, ik);
+                            if (!ok || 2 * j >= sub) continue;
+                            if (2 * j + 2 < sub) issue_s(x, x, ik);
+                            else if (leader) w4p::tc_commit(&o_done[x]);
                         }
                         if (!ok) break;
                         free_slot(iv);
@@ -672,31 +783,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 } else {
                     // one tile: A takes the even blocks, B the odd ones
-                    const int nb = nb0 + nb1;
-                    for (int x = 0; x < min(2, nb) && ok; ++x) {
+                    const int nb = nb0 + nb1, subs = sub0 + sub1;
+                    for (int k = 0; k < min(2, nb) && ok; ++k) {
                         ok = wait_bit(full, full_ph, pos % S);
                         if (!ok) break;
                         w4p::tc_fence_after();
-                        issue_s(x, 0, pos);
+                        issue_s(k, 0, pos);
                         free_slot(pos);
                         ++pos;
                     }
                     if (leader && nb <= 2) w4p::tc_commit(q_empty);
                     for (int k = 0; k < nb && ok; ++k) {
-                        const int x = k & 1;
-                        ok = k >= mfirst ? wait_bit(fixed, fixed_ph, pos % S) : wait_bit(full, full_ph, pos % S);
-                        ok = ok && wait_p(x);
+                        const int x = k & 1, iv = pos, ik = pos + 1;
+                        ok = k >= mfirst ? wait_bit(fixed, fixed_ph, iv % S) : wait_bit(full, full_ph, iv % S);
+                        if (ok && k + 2 < nb) ok = wait_bit(full, full_ph, ik % S);
                         if (!ok) break;
-                        w4p::tc_fence_after();
-                        issue_o(x, pos, k < 2);
-                        free_slot(pos);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if (!ok || 2 * k + h >= subs) continue;
+                            ok = wait_p(x, h);
+                            if (!ok) continue;
+                            w4p::tc_fence_after();
+                            issue_o(x, h, iv, k < 2 && h == 0);
+                        }
+                        if (!ok) break;
+                        if (k + 2 < nb) issue_s(x, 0, ik);
+                        else if (leader) w4p::tc_commit(&o_done[x]);
+                        if (!ok) break;
+                        free_slot(iv);
                         ++pos;
                         if (k + 2 < nb) {
-                            ok = wait_bit(full, full_ph, pos % S);
-                            if (!ok) break;
-                            w4p::tc_fence_after();
-                            issue_s(x, 0, pos);
-                            free_slot(pos);
+                            free_slot(ik);
                             ++pos;
                             if (leader && k + 3 == nb) w4p::tc_commit(q_empty);
                         }
@@ -707,55 +824,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (leader) w4p::tc_commit(all_done);
             (void)mbar_wait(all_done, 0);
             __syncwarp();
-        } else {
-            // ---------------------------------------------------------- V of masked blocks
-            const int t = (warp - 10) * 32 + lane;
-            uint32_t raw_ph = 0;
-            int base = 0;
-            bool ok = true;
-            for (int n = 0; ok && take(n, ok); ++n) {
-                Work* w = slot(n);
-                const bool pair = p.tiles == 2;
-                const int nb = pair ? max(w->nb0, w->nb1) : w->nb0 + w->nb1;
-                for (int j = w->mfirst; j < nb; ++j) {
-                    // ring position of V_j: behind the K tiles that lead it
-                    const int lead = pair ? 1 : min(2, nb);
-                    const int s = (base + j + min(j + lead, nb)) % S;
-                    ok = all(wait_or_abort(&raw[s], (raw_ph >> s) & 1u, abort_flag));
-                    if (!ok) break;
-                    raw_ph ^= 1u << s;
-                    const int left = w->nk - (w->b0 + j) * kKeys;   // keys of the block that the sequence has
-                    unsigned char* v = smem + C::ring + s * C::kv_tile;
-                    constexpr uint32_t kExp = BF16 ? 0x7F807F80u : 0x7C007C00u;
-                    constexpr uint32_t kOne = BF16 ? 0x00800080u : 0x04000400u;
-                    bool any = false;
-#pragma unroll 4
-                    for (int q = t; q < NC * kKeys * 8; q += 64) {
-                        uint4* at = reinterpret_cast<uint4*>(v + q * 16);
-                        const uint4 d = *at;
-                        uint32_t e[4] = {d.x, d.y, d.z, d.w};
-                        // an exponent of all ones carries into the sign's place
-                        uint32_t hit = 0;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) hit |= (e[k] & kExp) + kOne;
-                        const bool behind = ((q >> 3) & (kKeys - 1)) >= left;
-                        if (!behind && !(hit & 0x80008000u)) continue;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint32_t bad = ((e[k] & kExp) + kOne) & 0x80008000u;
-                            e[k] = behind ? 0u : e[k] & ~((bad >> 15) * 0xFFFFu);
-                        }
-                        *at = make_uint4(e[0], e[1], e[2], e[3]);
-                        any |= !behind;
-                    }
-                    if (any) *reinterpret_cast<volatile int*>(&w->poison) = 1;
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&fixed[s]);
-                }
-                base += 2 * nb;
-                release(n);
-            }
         }
     } else {
         // -------------------------------------------------------------- softmax, one row a thread
@@ -764,50 +832,106 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int x = warp >> 2;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t ts = tmem + lanes + 128 * x, to = tmem + lanes + 256 + DP * x;
-        int cnt = 0, ones = 0;   // S tiles, one-tile items so far
+        int ones = 0;                    // one-tile items so far
+        const int rg = (threadIdx.x & (kRows - 1)) / p.group;
+        int base = 0;                    // ring position of the item's K_0
+        uint32_t raw_ph = 0;             // a bit a stage
+        uint32_t s_ph = 0, o_ph = 0;     // parities of the next S, of the next item's O
         bool ok = true;
+        const bool pair = p.tiles == 2;
         for (int item = 0; ok && take(item, ok); ++item) {
-        const volatile Work* const ws = slot(item);
+        volatile Work* const ws = slot(item);
         float m = -INFINITY, l = 0.0f;   // reference maximum of the raw scores, sum of the weights
-        const int n = x ? ws->nb1 : ws->nb0;
-        const int mfirst = ws->mfirst;
-        const Row mine = row_of(p, ws, x);
+        const int n = x ? ws->sub1 : ws->sub0;
+        const int common = ws->common;
+        const Row mine = row_of(p, ws, x, rg);
         const int limit = mine.limit - ws->b0 * kKeys;   // in the item's keys
         const bool busy = __any_sync(0xffffffffu, mine.live);
-        const bool pair = p.tiles == 2;
-        for (int t = 0; t < n; ++t, ++cnt) {
-            const int j = pair ? t : 2 * t + x;   // key block
-            ok = all(wait_or_abort(&s_full[x], cnt & 1, abort_flag));
+        // blocks of the item (of both tiles), the next one whose V may need a look
+        const int nb = pair ? blocks_of_subs(max(ws->sub0, ws->sub1)) : blocks_of_subs(ws->sub0) + blocks_of_subs(ws->sub1);
+        int look = common / kKeys;
+        auto look_until = [&](int j) {   // V of all blocks up to j
+            for (; look <= j && look < nb && ok; ++look) {
+                const int s = (base + look + min(look + (pair ? 1 : min(2, nb)), nb)) % S;
+                ok = all(wait_or_abort(&raw[s], (raw_ph >> s) & 1u, abort_flag));
+                raw_ph ^= 1u << s;
+                if (!ok) break;
+                // rows from `from` on are not seen by every row, rows from `left` on by none
+                const int from = max(0, common - look * kKeys), left = ws->seen - look * kKeys;
+                unsigned char* v = smem + C::ring + s * C::kv_tile;
+                constexpr uint32_t kExp = BF16 ? 0x7F807F80u : 0x7C007C00u;
+                constexpr uint32_t kOne = BF16 ? 0x00800080u : 0x04000400u;
+                bool any = false;
+                for (int q = 8 * from + threadIdx.x; q < 8 * kKeys; q += 256) {
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) {
+                        uint4* at = reinterpret_cast<uint4*>(v + c * kKeys * 128 + q * 16);
+                        if (q >= 8 * left) {
+                            *at = make_uint4(0u, 0u, 0u, 0u);
+                            continue;
+                        }
+                        const uint4 d = *at;
+                        uint32_t e[4] = {d.x, d.y, d.z, d.w}, hit = 0;
+                        // an exponent of all ones carries into the sign's place
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) hit |= (e[k] & kExp) + kOne;
+                        if (!(hit & 0x80008000u)) continue;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) e[k] &= ~(((((e[k] & kExp) + kOne) & 0x80008000u) >> 15) * 0xFFFFu);
+                        *at = make_uint4(e[0], e[1], e[2], e[3]);
+                        any = true;
+                    }
+                }
+                if (any) ws->poison = 1;
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&fixed[s]);
+            }
+        };
+        for (int u = 0; u < n; u += 2) {
+            const int key = pair ? kSub * u : kKeys * (u + x);   // first key of the block
+            look_until(key / kKeys);
             if (!ok) break;
-            if (busy) {   // (P of rows that are no tokens may be anything)
+            ok = all(wait_or_abort(&s_full[x], s_ph, abort_flag));
+            if (!ok) break;
+            s_ph ^= 1u;
+            if (!busy) {   // (P of rows that are no tokens may be anything)
+                if (lane == 0) {
+                    mbar_arrive(&p_full[2 * x]);
+                    if (u + 1 < n) mbar_arrive(&p_full[2 * x + 1]);
+                }
+                continue;
+            }
             w4p::tc_fence_after();
             uint32_t sr[8][16];
 #pragma unroll
             for (int c = 0; c < 8; ++c) tmem_ld16_async(ts + 16 * c, sr[c]);
             tmem_wait_ld();
-            if (j >= mfirst) {
-                const int lim = limit - j * kKeys;
+            if (key + kKeys > common) {
+                const int lim = limit - key;
 #pragma unroll
                 for (int c = 0; c < 8; ++c)
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
                         if (16 * c + i >= lim) sr[c][i] = 0xFF800000u;
             }
-            float bm = -INFINITY;
+            // four chains: one would be 64 dependent instructions long
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
             for (int c = 0; c < 8; ++c)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) bm = fmaxf(bm, __uint_as_float(sr[c][i]));
-            // (NaN compares false: such a row keeps its reference and ends as NaN)
+                for (int i = 0; i < 8; ++i)
+                    mx[i & 3] = max3(mx[i & 3], __uint_as_float(sr[c][2 * i]), __uint_as_float(sr[c][2 * i + 1]));
+            const float bm = max3(max3(mx[0], mx[1], mx[2]), mx[3], mx[3]);
+            // A NaN or +infinity among the scores makes the row NaN.  NaN compares false below:
+            // the row keeps its reference.
+            if (!(bm < INFINITY)) l = NAN;
             const bool raise = m == -INFINITY ? bm > m : (bm - m) * p.scale_log2 > kLazy;
             if (__any_sync(0xffffffffu, raise)) {
                 const float nm = raise ? bm : m;
                 const float f = raise ? ex2((m - nm) * p.scale_log2) : 1.0f;
-                if (t > 0) {
-                    // O is complete up to the last block (its P V must be done), then rescaled
-                    ok = all(wait_or_abort(&o_done[x], (cnt - 1) & 1, abort_flag));
-                    if (!ok) break;
-                    w4p::tc_fence_after();
+                if (u > 0) {
+                    // (O is complete up to the last block: this S was issued behind its P V)
 #pragma unroll
                     for (int c = 0; c < DP / 16; ++c) {
                         uint32_t o[16];
@@ -817,35 +941,44 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
                         tmem_st16(to + 16 * c, o);
                     }
-                    tmem_wait_st();
                 }
-                l *= f;
+                l *= f;   // (NaN stays NaN)
                 m = nm;
             }
-            const float base = m == -INFINITY ? 0.0f : kShift - m * p.scale_log2;
+            const float shift = m == -INFINITY ? 0.0f : kShift - m * p.scale_log2;
             float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t pr[16];
+            for (int h = 0; h < 2; ++h) {
+                if (h == 1 && u + 1 >= n) break;   // the item's last block may be half
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float a = ex2(fmaf(__uint_as_float(sr[2 * c + (i >> 3)][2 * (i & 7)]), p.scale_log2, base));
-                    const float b = ex2(fmaf(__uint_as_float(sr[2 * c + (i >> 3)][2 * (i & 7) + 1]), p.scale_log2, base));
-                    sum[2 * (i & 1)] += a;
-                    sum[2 * (i & 1) + 1] += b;
-                    pr[i] = pack2<BF16>(a, b);
+                for (int c = 2 * h; c < 2 * h + 2; ++c) {
+                    uint32_t pr[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        float a = __uint_as_float(sr[2 * c + (i >> 3)][2 * (i & 7)]);
+                        float b = __uint_as_float(sr[2 * c + (i >> 3)][2 * (i & 7) + 1]);
+                        fma2_to(a, b, p.scale_log2, shift);
+                        a = ex2(a);
+                        b = ex2(b);
+                        add2_to(sum[2 * (i & 1)], sum[2 * (i & 1) + 1], a, b);
+                        pr[i] = pack2<BF16>(a, b);
+                    }
+                    tmem_st16(ts + 16 * c, pr);
                 }
-                tmem_st16(ts + 16 * c, pr);
+                tmem_wait_st();
+                w4p::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[2 * x + h]);
             }
             l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            tmem_wait_st();
-            w4p::tc_fence_before();
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[x]);
         }
+        if (ok) look_until(nb);
+        base += 2 * nb;
         // the item's output
-        if (n > 0 && ok) ok = all(wait_or_abort(&o_done[x], (cnt - 1) & 1, abort_flag));
+        if (n > 0 && ok) {
+            ok = all(wait_or_abort(&o_done[x], o_ph, abort_flag));
+            o_ph ^= 1u;
+        }
         if (!ok) break;
         // weights of this warp's O and, with one tile, of the other's O of the same rows
         float own = 1.0f, other = 0.0f;
@@ -866,95 +999,113 @@ __global__ void __launch_bounds__(kThreads, 1)
         w4p::tc_fence_after();
         if (busy) {
             // read again: kept in registers through the loop, these would not fit
-            const Row r = row_of(p, ws, x);
+            const Row r = row_of(p, ws, x, rg);
             const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
             own *= inv;
             other *= inv;
-            const int n_other = pair ? 0 : x ? ws->nb0 : ws->nb1;
-            const bool bad = ws->poison != 0;
-            const int first = (ws->b0 + mfirst) * kKeys;   // keys whose V was looked through
-            const int last = min(r.limit, (ws->b0 + n + n_other) * kKeys);
-            const unsigned short* vrow = reinterpret_cast<const unsigned short*>(p.V) + (size_t)ws->k0 * p.ldv +
-                                         (size_t)ws->hk * p.hsv;
+            const int n_other = pair ? 0 : x ? ws->sub0 : ws->sub1;
+            const int head = ws->hk * p.group + (threadIdx.x & (kRows - 1)) - rg * p.group;
             const bool part = ws->part >= 0;
             // row offsets in the output, and where the rows of this warp that are tokens lie
             const size_t tok = (size_t)(ws->q0 + r.tok);
             const size_t prow = (size_t)ws->part * kRows + (threadIdx.x & (kRows - 1));
-            const size_t at = part ? prow * p.dim : tok * p.ldo + (size_t)r.head * p.hso;
+            const size_t at = part ? prow * p.dim : tok * p.ldo + (size_t)head * p.hso;
             const unsigned live = __ballot_sync(0xffffffffu, r.live);
             unsigned char* st = smem + C::out + warp * 4096;
+            // O columns [c, c + 32) of this row, weighted
+            auto load_o = [&](int c, uint32_t (&o)[2][16]) {
+                if (n > 0) {
+                    tmem_ld16_async(to + c, o[0]);
+                    tmem_ld16_async(to + c + 16, o[1]);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i >> 4][i & 15] = __float_as_uint(__uint_as_float(o[i >> 4][i & 15]) * own);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i >> 4][i & 15] = 0u;
+                }
+                if (n_other > 0) {
+                    uint32_t o2[2][16];
+                    tmem_ld16_async(to + (x ? -DP : DP) + c, o2[0]);
+                    tmem_ld16_async(to + (x ? -DP : DP) + c + 16, o2[1]);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        o[i >> 4][i & 15] = __float_as_uint(
+                            fmaf(__uint_as_float(o2[i >> 4][i & 15]), other, __uint_as_float(o[i >> 4][i & 15])));
+                }
+            };
             // 128 bytes of each row at a time (64 16-bit or 32 fp32 columns) through shared
-            // memory, 16-byte pieces swizzled by row: a warp then writes whole 128-byte lines
-            // of four rows instead of 16 bytes of 32
+            // memory, 16-byte pieces swizzled by row: from there the tensor store takes 32 whole
+            // rows, or the warp writes whole 128-byte lines of four rows at a time.
             const int cols = part ? 32 : 64;
+            const bool whole = p.tma_out && !part && live == 0xffffffffu;
+            size_t to_row[8];
+            if (!whole) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) to_row[k] = __shfl_sync(0xffffffffu, (unsigned long long)at, 4 * k + (lane >> 3));
+            }
 #pragma unroll 1
             for (int c0 = 0; c0 < p.dim; c0 += cols) {
                 if (!pair && (c0 / cols & 1) != x) continue;   // one tile: the two warps of a row take turns
-#pragma unroll 1
-                for (int h = 0; h < cols; h += 16) {
-                    uint32_t o[16];
-                    __syncwarp();
-                    if (n > 0) {
-                        tmem_ld16_async(to + c0 + h, o);
-                        tmem_wait_ld();
-                    }
+                if (lane == 0) tma_store_read();   // the last store has read its bytes
+                __syncwarp();
+                uint32_t o[2][16];
+                if (part) {
+                    load_o(c0, o);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        o[i] = n > 0 && l != 0.0f ? __float_as_uint(__uint_as_float(o[i]) * own) : 0u;
-                    if (n_other > 0) {
-                        uint32_t o2[16];
-                        tmem_ld16_async(to + (x ? -DP : DP) + c0 + h, o2);
-                        tmem_wait_ld();
+                    for (int q = 0; q < 8; ++q)
+                        *reinterpret_cast<uint4*>(st + lane * 128 + ((q ^ (lane & 7)) << 4)) =
+                            make_uint4(o[q >> 2][4 * (q & 3)], o[q >> 2][4 * (q & 3) + 1], o[q >> 2][4 * (q & 3) + 2],
+                                       o[q >> 2][4 * (q & 3) + 3]);
+                } else {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (l != 0.0f) o[i] = __float_as_uint(fmaf(__uint_as_float(o2[i]), other, __uint_as_float(o[i])));
-                    }
-                    if (bad) {
-                        // non-finite values that the spare warps took out of V, for the rows that see them
-                        for (int j = first; j < last; ++j) {
+                    for (int h = 0; h < 2; ++h) {
+                        load_o(c0 + 32 * h, o);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                if (c0 + h + i >= p.dim) break;
-                                const uint32_t b = vrow[(size_t)j * p.ldv + c0 + h + i];
-                                const float f = BF16 ? __uint_as_float(b << 16) : __half2float(__ushort_as_half((unsigned short)b));
-                                if (!isfinite(f)) o[i] = __float_as_uint(__uint_as_float(o[i]) + f);
-                            }
-                        }
-                    }
-                    if (part) {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            *reinterpret_cast<uint4*>(st + lane * 128 + (((h / 4 + q) ^ (lane & 7)) << 4)) =
-                                make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < 2; ++q) {
+                        for (int q = 0; q < 4; ++q) {
                             uint32_t e[4];
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
-                                e[k] = pack2<BF16>(__uint_as_float(o[8 * q + 2 * k]), __uint_as_float(o[8 * q + 2 * k + 1]));
-                            *reinterpret_cast<uint4*>(st + lane * 128 + (((h / 8 + q) ^ (lane & 7)) << 4)) =
+                                e[k] = pack2<BF16>(__uint_as_float(o[q >> 1][8 * (q & 1) + 2 * k]),
+                                                   __uint_as_float(o[q >> 1][8 * (q & 1) + 2 * k + 1]));
+                            *reinterpret_cast<uint4*>(st + lane * 128 + (((4 * h + q) ^ (lane & 7)) << 4)) =
                                 make_uint4(e[0], e[1], e[2], e[3]);
                         }
                     }
                 }
+                if (ws->poison != 0) {
+                    const int first = ws->b0 * kKeys + common, last = min(r.limit, ws->b0 * kKeys + (n + n_other) * kSub);
+                    repair_row<BF16>(st + lane * 128, lane, part, c0, min(cols, p.dim - c0),
+                                     reinterpret_cast<const unsigned short*>(p.V) + (size_t)(ws->k0 + first) * p.ldv +
+                                         (size_t)ws->hk * p.hsv, p.ldv, last - first);
+                    __syncwarp();
+                }
+                if (whole) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) tma_store_3d(&tmap_o, st, c0, ws->hk * p.group, (int)tok);
+                    continue;
+                }
                 __syncwarp();
+                const int col = c0 + (part ? 4 : 8) * (lane & 7);
+                uint4 d[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    d[k] = *reinterpret_cast<const uint4*>(st + (4 * k + (lane >> 3)) * 128 +
+                                                           (((lane & 7) ^ ((4 * k + (lane >> 3)) & 7)) << 4));
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                    const int row = 4 * k + (lane >> 3), q = lane & 7;
-                    const size_t to_row = __shfl_sync(0xffffffffu, (unsigned long long)at, row);
-                    const uint4 d = *reinterpret_cast<const uint4*>(st + row * 128 + ((q ^ (row & 7)) << 4));
-                    const int col = c0 + (part ? 4 : 8) * q;
-                    if (!((live >> row) & 1u) || col >= p.dim) continue;
-                    if (part) *reinterpret_cast<uint4*>(p.part_o + to_row + col) = d;
-                    else *reinterpret_cast<uint4*>(reinterpret_cast<unsigned short*>(p.O) + to_row + col) = d;
+                    if (!((live >> (4 * k + (lane >> 3))) & 1u) || col >= p.dim) continue;
+                    if (part) *reinterpret_cast<uint4*>(p.part_o + to_row[k] + col) = d[k];
+                    else *reinterpret_cast<uint4*>(reinterpret_cast<unsigned short*>(p.O) + to_row[k] + col) = d[k];
                 }
                 __syncwarp();
             }
             const float v = l == 0.0f ? -INFINITY : m * p.scale + (logf(l) - kShift * 0.69314718055994531f);
             if (r.live && (pair || x == 0)) {
                 if (part) p.part_lse[prow] = v;
-                else if (p.lse) p.lse[tok * p.heads + r.head] = v;
+                else if (p.lse) p.lse[tok * p.heads + head] = v;
             }
         }
         if (!pair) {
@@ -968,6 +1119,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         release(item);
         }
+        if (lane == 0) tma_store_done();
     }
     w4p::tc_fence_before();
     __syncthreads();
@@ -988,25 +1140,30 @@ __global__ void __launch_bounds__(256) combine_kernel(const AttnParams p) {
     const size_t row = (size_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     if (row >= (size_t)p.total_q * p.heads) return;
     const int tok = (int)(row / p.heads), head = (int)(row % p.heads);
-    // the token's sequence: the last one that starts at or before it
-    int b = 0;
-    for (int hi = p.batch; p.cu_q && hi - b > 1;) {
-        const int mid = (b + hi) / 2;
-        if (__ldg(p.cu_q + mid) <= tok) b = mid;
-        else hi = mid;
+    // the token's sequence, the blocks of the sequences before it and of all
+    Work w = {};
+    long long before = 0, total = 0;
+    bool found = false;
+    for (int b0 = 0; b0 < p.batch; b0 += 32) {
+        Seqs s;
+        s.load(p, b0 + lane);
+        const long long size = b0 + lane < p.batch ? List::size(p, s) : 0;
+        const unsigned here = __ballot_sync(0xffffffffu, tok >= s.q0 && tok < s.q0 + s.nq);
+        if (here && !found) {
+            const int src = __ffs(here) - 1;
+            s.give(w, src);
+            before = total + List::sum(lane < src ? size : 0);
+            found = true;
+        }
+        total += List::sum(size);
     }
-    int q0, nq, k0, nk;
-    bool bad = false;
-    seq_bounds(p.cu_q, p.total_q, b, q0, nq, bad);
-    seq_bounds(p.cu_k, p.total_k, b, k0, nk, bad);
-    if (tok < q0 || tok >= q0 + nq) return;   // behind the last sequence: left as it is
-    const int tile = (tok - q0) / p.tpt, hk = head / p.group, nb = List::blocks_of(nk);
-    const long long total = List::before(p, p.batch, lane);
-    const long long u = List::before(p, b, lane) + ((long long)tile * p.kv_heads + hk) * nb;
+    if (!found) return;   // behind the last sequence: left as it is
+    const int tile = (tok - w.q0) / p.tpt, hk = head / p.group, nb = List::blocks_of(w.nk);
+    const long long u = before + ((long long)tile * p.kv_heads + hk) * nb;
     const int first = List::cta_of(p, total, u), last = List::cta_of(p, total, u + nb - 1);
     if (first == last) return;
     // part of CTA c: its last (place 1) where it starts the item, its first (place 0) otherwise
-    const int in_tile = (tok - q0 - tile * p.tpt) * p.group + head % p.group;
+    const int in_tile = (tok - w.q0 - tile * p.tpt) * p.group + head % p.group;
     auto place = [&](int c) {
         return (size_t)(2 * c + (c == first ? 1 : 0)) * kRows + in_tile;
     };

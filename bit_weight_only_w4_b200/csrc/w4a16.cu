@@ -1535,8 +1535,8 @@ AttnPlan attention_plan(int64_t batch, int32_t heads, int32_t kv_heads, int32_t 
 }
 
 template <bool BF16, int DP>
-w4_status launch_attention(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const w4t::AttnParams& p,
-                           long long grid, int dev, cudaStream_t stream) {
+w4_status launch_attention(const CUtensorMap (&maps)[4], const w4t::AttnParams& p, long long grid, int dev,
+                           cudaStream_t stream) {
     static std::once_flag flags[kMaxDevices];
     const auto k = w4t::attention_kernel<BF16, DP>;
     if (!ensure_smem(k, w4t::Cfg<DP>::bytes, flags, dev)) return W4_ERR_CUDA;
@@ -1558,7 +1558,7 @@ w4_status launch_attention(const CUtensorMap& mq, const CUtensorMap& mk, const C
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, k, mq, mk, mv, p) != cudaSuccess) return W4_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, k, maps[0], maps[1], maps[2], maps[3], p) != cudaSuccess) return W4_ERR_CUDA;
     if (p.part_o) {
         cfg.gridDim = dim3((unsigned)(((size_t)p.total_q * p.heads + 7) / 8));
         cfg.blockDim = dim3(256);
@@ -1637,19 +1637,24 @@ extern "C" w4_status w4_prompt_attention(const w4_attention* a, w4_dtype dtype, 
     p.scale = a->scale;
     p.scale_log2 = a->scale * 1.44269504088896341f;
     const bool bf16 = dtype == W4_BF16;
-    CUtensorMap mq, mk, mv;
+    CUtensorMap maps[4];   // Q, K, V, O
     // without keys nothing is loaded, but a map needs an address
     const void* K = a->k_tokens > 0 ? a->K : a->Q;
     const void* V = a->k_tokens > 0 ? a->V : a->Q;
     const int64_t kt = std::max<int64_t>(1, a->k_tokens);
-    if (!make_head_map(&mq, a->Q, bf16, a->head_dim, a->heads, a->q_tokens, a->q_head_stride, a->q_token_stride, p.group, p.tpt) ||
-        !make_head_map(&mk, K, bf16, a->head_dim, a->kv_heads, kt, a->k_head_stride, a->k_token_stride, 1, w4t::kKeys) ||
-        !make_head_map(&mv, V, bf16, a->head_dim, a->kv_heads, kt, a->v_head_stride, a->v_token_stride, 1, w4t::kKeys))
+    if (!make_head_map(&maps[0], a->Q, bf16, a->head_dim, a->heads, a->q_tokens, a->q_head_stride, a->q_token_stride, p.group, p.tpt) ||
+        !make_head_map(&maps[1], K, bf16, a->head_dim, a->kv_heads, kt, a->k_head_stride, a->k_token_stride, 1, w4t::kKeys) ||
+        !make_head_map(&maps[2], V, bf16, a->head_dim, a->kv_heads, kt, a->v_head_stride, a->v_token_stride, 1, w4t::kKeys))
+        return W4_ERR_CUDA;
+    // a softmax warp's 32 rows hold whole tokens: it stores them by TMA
+    p.tma_out = 32 % p.group == 0 ? 1 : 0;
+    if (!make_head_map(&maps[3], a->O, bf16, a->head_dim, a->heads, a->q_tokens, a->o_head_stride, a->o_token_stride,
+                       p.tma_out ? p.group : 1, p.tma_out ? 32 / p.group : 1))
         return W4_ERR_CUDA;
     cudaStream_t strm = as_stream(stream);
     if (a->head_dim <= 64)
-        return bf16 ? launch_attention<true, 64>(mq, mk, mv, p, L.grid, dev, strm)
-                    : launch_attention<false, 64>(mq, mk, mv, p, L.grid, dev, strm);
-    return bf16 ? launch_attention<true, 128>(mq, mk, mv, p, L.grid, dev, strm)
-                : launch_attention<false, 128>(mq, mk, mv, p, L.grid, dev, strm);
+        return bf16 ? launch_attention<true, 64>(maps, p, L.grid, dev, strm)
+                    : launch_attention<false, 64>(maps, p, L.grid, dev, strm);
+    return bf16 ? launch_attention<true, 128>(maps, p, L.grid, dev, strm)
+                : launch_attention<false, 128>(maps, p, L.grid, dev, strm);
 }
