@@ -35,16 +35,37 @@ W4_DEV float load_elem(const void* p, int dtype, size_t i) {
 
 // One fp32 activation.  The exponential is the hardware's 2^x (a few ulp of fp32 over the
 // range where the result is not negligible): far below the rounding to a 16-bit Y.
-//   silu      x / (1 + e^-x)
-//   gelu      x Phi(x) = x/2 erfc(-x / sqrt 2)        (erfc keeps the negative tail's digits)
-//   gelu_tanh x/2 (1 + tanh u) = x / (1 + e^-2u),  u = sqrt(2/pi) (x + 0.044715 x^3)
-W4_DEV float activate(int act, float x) {
-    if (act == kActNone) return x;
-    if (act == kActRelu) return x < 0.0f ? 0.0f : x;   // NaN stays NaN
-    if (act == kActGelu) return 0.5f * x * erfcf(-0.70710678118654752f * x);
-    const float u = act == kActSilu ? x : 1.5957691216057308f * fmaf(0.044715f * x * x, x, x);
-    // for e^-u beyond 2^126 the quotient is below 2^-100: __fdividef's zero there is right
-    return __fdividef(x, 1.0f + __expf(-u));
+//   none, relu  x, not below `low` (-inf, 0; NaN stays NaN)
+//   silu        x / (1 + e^-x)
+//   gelu_tanh   x/2 (1 + tanh w) = x / (1 + e^-2w),  2w = sqrt(8/pi) (x + 0.044715 x^3): the
+//               same form as silu with another argument
+//   gelu        x Phi(x) = x/2 erfc(-x / sqrt 2)      (erfc keeps the negative tail's digits)
+enum : int { kKindClamp = 0, kKindSigmoid = 1, kKindErf = 2 };
+template <int K>
+struct KindOf {
+    static constexpr int value = K;
+};
+
+struct Act {
+    int kind;
+    float a, c;   // clamp: a = low; sigmoid: argument x (a + c x^2)
+    W4_DEV explicit Act(int act) {
+        kind = act == kActNone || act == kActRelu ? kKindClamp : act == kActGelu ? kKindErf : kKindSigmoid;
+        a = act == kActNone ? -INFINITY : act == kActRelu ? 0.0f : act == kActSilu ? 1.0f : 1.5957691216057308f;
+        c = act == kActGeluTanh ? 1.5957691216057308f * 0.044715f : 0.0f;
+    }
+    template <int K>
+    W4_DEV float apply(float x) const {
+        if constexpr (K == kKindClamp) return x < a ? a : x;
+        else if constexpr (K == kKindErf) return 0.5f * x * erfcf(-0.70710678118654752f * x);
+        // for e^-u beyond 2^126 the quotient is below 2^-100: __fdividef's zero there is right
+        else return __fdividef(x, 1.0f + __expf(-x * fmaf(c * x, x, a)));
+    }
+};
+W4_DEV float activate(const Act& act, float x) {
+    if (act.kind == kKindSigmoid) return act.apply<kKindSigmoid>(x);
+    if (act.kind == kKindErf) return act.apply<kKindErf>(x);
+    return act.apply<kKindClamp>(x);
 }
 
 }  // namespace w4e

@@ -260,7 +260,94 @@ W4_DEV void load_staged8(const float* src, float (&v)[8]) {
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
 
-template <bool BF16, int WM, bool EPI>
+// Drain of one tile with an ungated epilogue and 16-bit output (and residual): bias and
+// activation on the registers; only 16-bit values cross shared memory, all global memory
+// moves in 16-byte pieces.  The residual is copied asynchronously into the staging buffer's
+// place of the output, where the thread of that output adds it in fp32 and writes the result
+// over it; the next block's is on its way meanwhile (two areas of kYChunk tokens of each
+// half), the first block's from the tile's start on.  Against fp32 staging with the residual
+// read on the way out: GELU, 1037 x 11008 x 4096, 172 -> 153 us; residual, 2048 x 4096 x
+// 14336, 326 -> 298 us.  Gated outputs stay with fp32 staging: exchanging gate and up between
+// lanes to halve what is staged took longer (2048 x 28672 x 4096: 583 us against 567).
+struct Drain16 {
+    static constexpr int kBlocks = BM / 2 / kYChunk;
+    static constexpr int PIECES = 2 * kYChunk * BN / 8 / 256;   // 16-byte pieces a thread moves a block
+    const PrefillParams& p;
+    const w4e::Epilogue& epi;
+    unsigned char* yt;
+    int n0, m0, t;   // first row and token of the tile, this thread of the 256
+
+    W4_DEV unsigned short* area(int ck) const {
+        return reinterpret_cast<unsigned short*>(yt) + (ck & 1) * 2 * kYChunk * BN;
+    }
+    // piece k of block ck: its token, first column; whether it is an output
+    W4_DEV bool where(int k, int ck, int& mm, int& col) const {
+        const int cc = t + 256 * k, m = cc / (BN / 8);
+        col = n0 + 8 * (cc % (BN / 8));
+        mm = m0 + (m / kYChunk) * (BM / 2) + ck * kYChunk + m % kYChunk;
+        return mm < p.M && col < p.N;
+    }
+    W4_DEV void fetch(int ck) const {
+        if (!epi.residual) return;
+#pragma unroll 1
+        for (int k = 0; k < PIECES; ++k) {
+            int mm, col;
+            if (where(k, ck, mm, col))
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(area(ck)) + 16u * (t + 256 * k)),
+                             "l"(reinterpret_cast<const unsigned short*>(epi.residual) + (size_t)mm * epi.ldr + col)
+                             : "memory");
+        }
+    }
+    W4_DEV void run(const float (&acc)[BM / 2], int row, int h, bool ok) const {
+        const float bias = (epi.bias && n0 + row < p.N) ? w4e::load_elem(epi.bias, epi.bias_dtype, n0 + row) : 0.0f;
+        const bool bf16 = p.out_dtype == 1;
+        const w4e::Act act(epi.act);
+#pragma unroll
+        for (int ck = 0; ck < kBlocks; ++ck) {
+            unsigned short* os = area(ck) + h * kYChunk * BN + row;
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            named_bar_sync(1, 256);   // the residual is there, the other area free
+            if (ck + 1 < kBlocks && ok) fetch(ck + 1);
+            auto put = [&](int i, float v) {
+                if (epi.residual) {
+                    const uint32_t b = os[i * BN];
+                    v += epi.res_dtype == 1 ? __uint_as_float(b << 16) : __half2float(__ushort_as_half((unsigned short)b));
+                }
+                os[i * BN] = bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
+            };
+            // (the kind of activation is the same for all: one test a block, not an element)
+            auto block = [&](auto kind) {
+#pragma unroll
+                for (int i = 0; i < kYChunk; ++i)
+                    put(i, act.template apply<decltype(kind)::value>(acc[ck * kYChunk + i] + bias));
+            };
+            if (ok) {
+                if (act.kind == w4e::kKindSigmoid) block(w4e::KindOf<w4e::kKindSigmoid>{});
+                else block(w4e::KindOf<w4e::kKindClamp>{});
+            }
+            named_bar_sync(1, 256);
+            if (ok) {
+#pragma unroll 1
+                for (int k = 0; k < PIECES; ++k) {
+                    int mm, col;
+                    if (where(k, ck, mm, col))
+                        *reinterpret_cast<uint4*>(reinterpret_cast<unsigned short*>(p.Y) + (size_t)mm * epi.ldy + col) =
+                            reinterpret_cast<const uint4*>(area(ck))[t + 256 * k];
+                }
+            }
+        }
+    }
+};
+
+// Epilogues of the prefill kernel.  Each is a kernel of its own: code of the other drain in
+// the same kernel cost the gated product 12 us of 567.
+enum : int {
+    kEpiNone = 0,
+    kEpiWide = 1,    // staged in fp32: gated, fp32 output or residual, erf
+    kEpiPlain = 2,   // Drain16
+};
+
+template <bool BF16, int WM, int EPI>
 W4_DEV void prefill_body(const CUtensorMap& tmap_x, const PrefillParams& p, const w4e::Epilogue& epi) {
     constexpr bool GIDX = WM == kWGidx;
     constexpr bool FP4 = WM == kWNvfp4 || WM == kWMxfp4;
@@ -551,6 +638,7 @@ W4_DEV void prefill_body(const CUtensorMap& tmap_x, const PrefillParams& p, cons
             const int n0 = (t % nbands) * BN, m0 = (t / nbands) * BM;
             const int n = n0 + row;
             const bool row_ok = n < p.N;
+            if constexpr (EPI == kEpiPlain) Drain16{p, epi, yt, n0, m0, 32 * e + lane}.fetch(0);
             float acc[BM / 2];
 #pragma unroll
             for (int i = 0; i < BM / 2; ++i) acc[i] = 0.0f;
@@ -579,11 +667,14 @@ W4_DEV void prefill_body(const CUtensorMap& tmap_x, const PrefillParams& p, cons
             // along N.  The next tile's MMAs proceed meanwhile.
             const int cpr = BN * esz / 16;               // 16-byte pieces per token row
             const int ncols = min(BN, p.N - n0);         // a multiple of 16 (N % 16 == 0)
-            if constexpr (EPI) {
-                // the same staging in fp32, bias added on the way in (one row a thread);
-                // activation, gate and residual on the way out, 8 outputs a thread
+            if constexpr (EPI == kEpiPlain) {
+                Drain16{p, epi, yt, n0, m0, 32 * e + lane}.run(acc, row, h, ok);
+            } else if constexpr (EPI == kEpiWide) {
+                // staged in fp32, bias added on the way in (one row a thread); activation, gate
+                // and residual on the way out, 8 outputs a thread
                 const float bias = (epi.bias && row_ok) ? w4e::load_elem(epi.bias, epi.bias_dtype, n) : 0.0f;
                 float* ys = reinterpret_cast<float*>(yt);
+                const w4e::Act act(epi.act);
                 const int pieces = epi.gated ? BN / 16 : BN / 8;
                 const int npc = min(BN, p.N - n0) / (epi.gated ? 16 : 8);
                 const int c0 = epi.gated ? n0 / 2 : n0;
@@ -601,16 +692,22 @@ W4_DEV void prefill_body(const CUtensorMap& tmap_x, const PrefillParams& p, cons
                             const int mm = m0 + (m / kYChunk) * (BM / 2) + ck * kYChunk + m % kYChunk;
                             if (mm >= p.M || pc >= npc) continue;
                             float v[8];
+                            load_staged8(ys + m * BN + (epi.gated ? 16 : 8) * pc, v);
+                            if (act.kind == w4e::kKindSigmoid) {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) v[i] = act.apply<w4e::kKindSigmoid>(v[i]);
+                            } else if (act.kind == w4e::kKindClamp) {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) v[i] = act.apply<w4e::kKindClamp>(v[i]);
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) v[i] = act.apply<w4e::kKindErf>(v[i]);
+                            }
                             if (epi.gated) {
                                 float up[8];
-                                load_staged8(ys + m * BN + 16 * pc, v);
                                 load_staged8(ys + m * BN + 16 * pc + 8, up);
 #pragma unroll
-                                for (int i = 0; i < 8; ++i) v[i] = w4e::activate(epi.act, v[i]) * up[i];
-                            } else {
-                                load_staged8(ys + m * BN + 8 * pc, v);
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) v[i] = w4e::activate(epi.act, v[i]);
+                                for (int i = 0; i < 8; ++i) v[i] *= up[i];
                             }
                             if (epi.residual) add_residual8(epi, (size_t)mm * epi.ldr + c0 + 8 * pc, v);
                             store8(p.Y, p.out_dtype, (size_t)mm * epi.ldy + c0 + 8 * pc, v);
@@ -659,14 +756,16 @@ W4_DEV void prefill_body(const CUtensorMap& tmap_x, const PrefillParams& p, cons
 template <bool BF16, int WM>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tmap_x, const PrefillParams p) {
-    prefill_body<BF16, WM, false>(tmap_x, p, w4e::Epilogue{});
+    prefill_body<BF16, WM, kEpiNone>(tmap_x, p, w4e::Epilogue{});
 }
 
-// The same product with an epilogue (a kernel of its own: the plain product keeps its code).
-template <bool BF16, int WM>
+// The same product with an epilogue (kernels of their own: the plain product keeps its code).
+// 2048 x 28672 x 4096 with SwiGLU 567 us (the product alone 536), 2048 x 4096 x 14336 with a
+// residual 297 us (281): the drain's excess over what the two tensor-memory buffers hide.
+template <bool BF16, int WM, int EPI>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_epi_kernel(const __grid_constant__ CUtensorMap tmap_x, const PrefillParams p, const w4e::Epilogue epi) {
-    prefill_body<BF16, WM, true>(tmap_x, p, epi);
+    prefill_body<BF16, WM, EPI>(tmap_x, p, epi);
 }
 
 // X'[m,k] = X[m,k] * s_inv[k], rounded to the activation type (for the prefill path,

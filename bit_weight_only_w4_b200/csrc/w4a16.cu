@@ -374,12 +374,12 @@ w4_status dispatch_decode(int mode, w4d::DecodeParams p, const void* X, unsigned
 }
 
 // ---------------------------------------------------------------- prefill launch plan
-template <bool BF16, int WM, bool EPI>
+template <bool BF16, int WM, int EPI>
 w4_status launch_prefill_kernel(const CUtensorMap& map, const w4p::PrefillParams& p, int dev,
                                 const w4e::Epilogue* epi, cudaStream_t stream) {
     static std::once_flag flags[kMaxDevices];
     const auto k = [] {
-        if constexpr (EPI) return w4p::prefill_epi_kernel<BF16, WM>;
+        if constexpr (EPI != w4p::kEpiNone) return w4p::prefill_epi_kernel<BF16, WM, EPI>;
         else return w4p::prefill_kernel<BF16, WM>;
     }();
     if (!ensure_smem(k, w4p::SmemLayout::bytes, flags, dev)) return W4_ERR_CUDA;
@@ -408,7 +408,7 @@ w4_status launch_prefill_kernel(const CUtensorMap& map, const w4p::PrefillParams
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     cudaError_t launched;
-    if constexpr (EPI) launched = cudaLaunchKernelEx(&cfg, k, map, p, *epi);
+    if constexpr (EPI != w4p::kEpiNone) launched = cudaLaunchKernelEx(&cfg, k, map, p, *epi);
     else launched = cudaLaunchKernelEx(&cfg, k, map, p);
     if (launched != cudaSuccess) return W4_ERR_CUDA;
     return launch_status();
@@ -419,9 +419,16 @@ template <bool BF16, int WM>
 w4_status launch_prefill(const CUtensorMap& map, const w4p::PrefillParams& p, int dev, cudaStream_t stream,
                          const w4e::Epilogue* epi = nullptr) {
     if constexpr (WM == w4p::kWInt4 || WM == w4p::kWGidx) {
-        if (epi) return launch_prefill_kernel<BF16, WM, true>(map, p, dev, epi, stream);
+        if (epi) {
+            // 16-bit values only, and no erfc (forty instructions an element, not to be unrolled
+            // over the accumulators): the drain that stages 16 bits
+            const bool wide = epi->gated || p.out_dtype == W4_F32 || (epi->residual && epi->res_dtype == W4_F32) ||
+                              epi->act == W4_ACT_GELU;
+            return wide ? launch_prefill_kernel<BF16, WM, w4p::kEpiWide>(map, p, dev, epi, stream)
+                        : launch_prefill_kernel<BF16, WM, w4p::kEpiPlain>(map, p, dev, epi, stream);
+        }
     }
-    return launch_prefill_kernel<BF16, WM, false>(map, p, dev, nullptr, stream);
+    return launch_prefill_kernel<BF16, WM, w4p::kEpiNone>(map, p, dev, nullptr, stream);
 }
 
 }  // namespace
