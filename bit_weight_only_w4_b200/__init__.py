@@ -712,12 +712,15 @@ def w4a16_gemm_epi(X, qweight, scales, zeros, group_size=128, bias=None, activat
         raise ValueError(f"unknown activation {activation!r} ({', '.join(k for k in _ACTIVATIONS if k)})")
     if bias is not None:
         _expect(bias, "bias", _dtypes()[:3], numel=N)
-    dev = _need_cuda(X, qweight, scales, zeros, g_idx, s_inv, bias, workspace, perm)
+    index = X.get_device()
+    for t in (X, qweight, scales, zeros, g_idx, s_inv, bias, workspace, perm):
+        if t is not None and (t.get_device() != index or index < 0 or not t.is_contiguous()):
+            _need_cuda(X, qweight, scales, zeros, g_idx, s_inv, bias, workspace, perm)   # names the reason
     n_out = N // 2 if gated else N
     xt = X.dtype
     if Y is None:
         yt = out_dtype or xt
-        Y = torch.empty((M, n_out), dtype=yt, device=dev)
+        Y = X.new_empty((M, n_out)) if yt is xt else X.new_empty((M, n_out), dtype=yt)
         ldy = n_out
     else:
         yt = Y.dtype
@@ -725,20 +728,21 @@ def w4a16_gemm_epi(X, qweight, scales, zeros, group_size=128, bias=None, activat
             raise TypeError(f"Y is {yt}, out_dtype {out_dtype}")
         ldy = _rows_of(Y, "Y", M, n_out)
     ldr = 0 if residual is None else _rows_of(residual, "residual", M, n_out)
-    if Y.device != dev or (residual is not None and residual.device != dev):
+    if Y.get_device() != index or (residual is not None and residual.get_device() != index):
         raise ValueError("tensors are on different devices")
     e = Epilogue(_ptr(bias), _ptr(residual), ldr, ldy, 0 if bias is None else _dtype_code(bias.dtype),
                  0 if residual is None else _dtype_code(residual.dtype), act, 1 if gated else 0)
     L = lib()
     if workspace is None and M > 0:
-        need = _workspace_size(dev.index, L.w4a16_workspace_bytes if perm is None else L.w4a16_workspace_bytes_perm,
+        need = _workspace_size(index, L.w4a16_workspace_bytes if perm is None else L.w4a16_workspace_bytes_perm,
                                M, N, K, group_size)
         if need > 0:
-            workspace = workspace_for(dev, need)
+            workspace = workspace_for(X.device, need)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    st = _on_device(dev.index, L.w4a16_gemm_epi, X.data_ptr(), _dtype_code(xt), M, N, K, qweight.data_ptr(),
+    st = _on_device(index, L.w4a16_gemm_epi, X.data_ptr(), _dtype_code(xt), M, N, K, qweight.data_ptr(),
                     scales.data_ptr(), _ptr(zeros), _ptr(g_idx), _ptr(perm), group_size, _ptr(s_inv), e, Y.data_ptr(),
-                    _dtype_code(yt), _ptr(workspace), ws_bytes, _stream_handle(stream, dev))
+                    _dtype_code(yt), _ptr(workspace), ws_bytes,
+                    torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
     if st:
         raise W4Error(st, "w4a16_gemm_epi")
     return Y
@@ -805,7 +809,7 @@ def w4_rope(X, positions, inv_freq, interleaved=False, mscale=1.0, Y=None, strea
     xt = X.dtype
     if Y is None:
         index = _cuda_index(X, positions, inv_freq)
-        Y = torch.empty(shape, dtype=xt, device=X.device)
+        Y = X.new_empty(shape)
         sy = (H * D, D)
     else:
         index = _cuda_index(X, positions, inv_freq, Y)
@@ -862,15 +866,14 @@ def w4_prompt_attention(Q, K, V, cu_seqlens=None, cu_seqlens_k=None, causal=True
                 raise ValueError(f"{name} must be a contiguous vector of batch+1 bounds, cu_seqlens_k with a "
                                  "cu_seqlens of the same length")
     index = _cuda_index(Q, K, V, cu_seqlens, cu_seqlens_k, O, workspace)
-    dev = Q.device
     if O is None:
-        O = torch.empty((Tq, H, D), dtype=dt, device=dev)
+        O = Q.new_empty((Tq, H, D))
         so = (H * D, D)
     else:
         os_, so = _heads_of(O, "O")
         if O.dtype is not dt or os_ != (Tq, H, D):
             _expect(O, "O", (dt,), shape=(Tq, H, D))
-    lse = torch.empty((Tq, H), dtype=torch.float32, device=dev) if return_lse else None
+    lse = Q.new_empty((Tq, H), dtype=torch.float32) if return_lse else None
     # w4_attention, packed at once (a ctypes structure of 24 fields takes longer to fill)
     a = _ATTENTION.pack(Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), 0 if lse is None else lse.data_ptr(),
                         0 if cu_seqlens is None else cu_seqlens.data_ptr(),
@@ -882,8 +885,11 @@ def w4_prompt_attention(Q, K, V, cu_seqlens=None, cu_seqlens_k=None, causal=True
         need = _workspace_size(index, L.w4_prompt_attention_workspace_bytes, batch, H, Hk, D, Tq, Tk)
         if need > 0:
             # of the stream that uses it, so that its next use is ordered behind this call
-            with torch.cuda.stream(stream):
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            if stream is None:
+                workspace = Q.new_empty(need, dtype=torch.uint8)
+            else:
+                with torch.cuda.stream(stream):
+                    workspace = Q.new_empty(need, dtype=torch.uint8)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     st = _on_device(index, L.w4_prompt_attention, a, _dtype_code(dt), _ptr(workspace), ws_bytes,
                     torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)

@@ -1363,22 +1363,27 @@ namespace {
 template <int DT, int E>
 w4_status launch_rope(w4r::RopeParams p, int sms, cudaStream_t stream) {
     const int half = p.rot / 2;
-    // an item is E pairs, two pieces; the tail behind rot is copied two pieces an item
+    // a piece is E pairs, two words; the tail behind rot is copied two words a piece
     p.per_head = half / E + (p.copy_tail ? (p.dim - p.rot + 2 * E - 1) / (2 * E) : 0);
-    // whole tokens fill a block; with few tokens the heads are split so that every SM works
-    const long long per_tok = (long long)p.heads * p.per_head;
-    p.tokens_per_block = (int)std::max<long long>(1, std::min<long long>(w4r::kMaxTokens, 256 / std::max<long long>(1, per_tok)));
+    if (p.per_head > w4r::kThreads) return W4_ERR_UNSUPPORTED;
+    // A thread takes its piece of the head through kBatch heads or more where there are tokens
+    // to fill the GPU, through one where there are few (then the heads are split among blocks,
+    // at least a warp's pieces each).
+    const int lanes = w4r::kThreads / p.per_head;   // (token, head lane) places of a block
+    const long long wide = (long long)p.tokens * ((p.heads + w4r::kBatch - 1) / w4r::kBatch);
     p.heads_per_block = p.heads;
-    const long long blocks = (p.tokens + p.tokens_per_block - 1) / p.tokens_per_block;
-    if (blocks < sms) {
-        // at least one warp's items a block
-        const int least = std::max(1, (32 + p.per_head - 1) / p.per_head);
-        const int want = (int)((p.heads * blocks + sms - 1) / sms);
-        p.heads_per_block = std::min(p.heads, std::max(least, want));
+    if (wide >= (long long)lanes * sms) {
+        p.head_lanes = std::min(lanes, (p.heads + w4r::kBatch - 1) / w4r::kBatch);
+    } else {
+        p.head_lanes = std::min(lanes, p.heads);
+        const int least = std::max(1, 32 / p.per_head);
+        const long long want = ((long long)p.heads * p.tokens + 2 * sms - 1) / (2 * sms);   // heads a block for two blocks an SM
+        p.head_lanes = (int)std::min<long long>(p.head_lanes, std::max<long long>(least, want));
+        p.heads_per_block = p.head_lanes;
     }
-    p.heads_per_block = std::min(p.heads_per_block, 65535);
-    const long long items = (long long)p.tokens_per_block * p.heads_per_block * p.per_head;
-    const int threads = (int)std::min<long long>(w4r::kMaxThreads, std::max<long long>(64, (items + 31) / 32 * 32));
+    p.tokens_per_block = std::max(1, std::min({w4r::kMaxTokens, lanes / p.head_lanes, p.tokens}));
+    const long long blocks = (p.tokens + p.tokens_per_block - 1) / p.tokens_per_block;
+    const int threads = w4r::kThreads;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)blocks, (unsigned)((p.heads + p.heads_per_block - 1) / p.heads_per_block));
     cfg.blockDim = dim3((unsigned)threads);
@@ -1402,7 +1407,7 @@ extern "C" w4_status w4_rope(const void* X, w4_dtype dtype, int64_t tokens, int3
     if (!valid_dtype(dtype) || tokens < 0 || heads < 0 || head_dim <= 0) return W4_ERR_INVALID_ARG;
     if (rot_dim < 2 || rot_dim % 2 != 0 || rot_dim > head_dim) return W4_ERR_INVALID_ARG;
     if ((interleaved != 0 && interleaved != 1) || !std::isfinite(mscale)) return W4_ERR_INVALID_ARG;
-    if (rot_dim / 2 > w4r::kMaxPairs || tokens > INT_MAX / 2 || heads > 65535 || head_dim > 65536) return W4_ERR_UNSUPPORTED;
+    if (rot_dim / 2 > w4r::kMaxPairs || tokens > INT_MAX / 2 || heads > 65535 || head_dim > 512) return W4_ERR_UNSUPPORTED;
     if (tokens == 0 || heads == 0) return W4_OK;
     const int esz = dtype_bytes(dtype);
     if (!X || !Y || !positions || !inv_freq) return W4_ERR_INVALID_ARG;

@@ -441,7 +441,7 @@ w4_status w4a16_gemm_epi(const void* X, w4_dtype act_dtype, int64_t M, int64_t N
  *   Y           device, the same type, strides of its own.  Y == X with equal strides rotates
  *               in place; any other overlap is not allowed
  *   positions   device int32 [tokens];  inv_freq  device fp64 [rot_dim/2]
- *   rot_dim     even, 2 .. head_dim, at most 512;  mscale finite
+ *   rot_dim     even, 2 .. head_dim;  head_dim at most 512;  mscale finite
  * Any stride and alignment of whole elements works; 16-byte alignment of the pointers and
  * strides, with head_dim and rot_dim/2 multiples of 16 bytes, is faster.  tokens == 0 or
  * heads == 0 is a no-op.  Asynchronous on `stream`; no workspace.
