@@ -261,6 +261,7 @@ struct List {
 
 // The items of a CTA's range, one after the other, by one warp.
 struct Walker {
+    long long total;       // blocks of the list
     long long at, end;     // next block of the list, end of the range
     long long ends;        // list index behind this lane's sequence
     Seqs seqs;             // 32 sequences, from b0 on
@@ -279,7 +280,7 @@ struct Walker {
     }
     W4_DEV void start(const AttnParams& p, int lane) {
         load(p, 0, 0, lane);
-        long long total = __shfl_sync(0xffffffffu, ends, 31);
+        total = __shfl_sync(0xffffffffu, ends, 31);
         for (int b = 32; b < p.batch; b += 32) {
             Seqs s;
             s.load(p, b + lane);
@@ -1130,40 +1131,46 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the parts of an item that ranges cut: O = sum_s e^(lse_s - lse) O_s, lse = log sum_s
-// e^lse_s over its parts s.  A warp a (token, head), four columns a lane; rows of items that no
-// range cut are already there.
+// e^lse_s over its parts s.  Block (c, y) joins rows 16 y .. of the item that CTA c's range
+// starts and does not end, if there is one (items that no range cuts are already there): two
+// rows a warp, four columns a lane.
+constexpr int kJoinRows = 16;
 template <bool BF16>
 __global__ void __launch_bounds__(256) combine_kernel(const AttnParams p) {
+    __shared__ Work s_work;
+    __shared__ int s_last;
     pdl_launch_dependents();
     pdl_wait();
-    const int lane = threadIdx.x & 31;
-    const size_t row = (size_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (row >= (size_t)p.total_q * p.heads) return;
-    const int tok = (int)(row / p.heads), head = (int)(row % p.heads);
-    // the token's sequence, the blocks of the sequences before it and of all
-    Work w = {};
-    long long before = 0, total = 0;
-    bool found = false;
-    for (int b0 = 0; b0 < p.batch; b0 += 32) {
-        Seqs s;
-        s.load(p, b0 + lane);
-        const long long size = b0 + lane < p.batch ? List::size(p, s) : 0;
-        const unsigned here = __ballot_sync(0xffffffffu, tok >= s.q0 && tok < s.q0 + s.nq);
-        if (here && !found) {
-            const int src = __ffs(here) - 1;
-            s.give(w, src);
-            before = total + List::sum(lane < src ? size : 0);
-            found = true;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, first = blockIdx.x;
+    if (warp == 0) {
+        Work w = {};
+        int last = first;
+        Walker walker;
+        walker.start(p, lane);
+        const long long total = walker.total, at = walker.end;   // first block of the next range
+        if (at < total && walker.at < at) {
+            walker.at = at;
+            walker.end = at + 1;
+            w = walker.next(p, lane);   // the item of that block
+            const long long start = at - w.b0;
+            if (w.b0 > 0 && start >= List::begin(p, total, first))
+                last = List::cta_of(p, total, start + List::blocks_of(w.nk) - 1);
         }
-        total += List::sum(size);
+        if (lane == 0) {
+            s_work = w;
+            s_last = last;
+        }
     }
-    if (!found) return;   // behind the last sequence: left as it is
-    const int tile = (tok - w.q0) / p.tpt, hk = head / p.group, nb = List::blocks_of(w.nk);
-    const long long u = before + ((long long)tile * p.kv_heads + hk) * nb;
-    const int first = List::cta_of(p, total, u), last = List::cta_of(p, total, u + nb - 1);
-    if (first == last) return;
+    __syncthreads();
+    const int last = s_last;
+    if (last == first) return;
+    const Work& w = s_work;
+    for (int in_tile = kJoinRows * blockIdx.y + warp; in_tile < kJoinRows * (blockIdx.y + 1); in_tile += 8) {
+    const int rg = in_tile / p.group, tok_in = w.tok + rg;
+    if (rg >= p.tpt || tok_in >= w.nq) continue;
+    const size_t tok = (size_t)(w.q0 + tok_in);
+    const int head = w.hk * p.group + in_tile - rg * p.group;
     // part of CTA c: its last (place 1) where it starts the item, its first (place 0) otherwise
-    const int in_tile = (tok - w.q0 - tile * p.tpt) * p.group + head % p.group;
     auto place = [&](int c) {
         return (size_t)(2 * c + (c == first ? 1 : 0)) * kRows + in_tile;
     };
@@ -1193,9 +1200,10 @@ __global__ void __launch_bounds__(256) combine_kernel(const AttnParams p) {
     }
     const float inv = nan ? NAN : sum > 0.0f ? 1.0f / sum : 0.0f;
     if (on)
-        *reinterpret_cast<uint2*>(reinterpret_cast<unsigned short*>(p.O) + (size_t)tok * p.ldo + (size_t)head * p.hso + 4 * lane) =
+        *reinterpret_cast<uint2*>(reinterpret_cast<unsigned short*>(p.O) + tok * p.ldo + (size_t)head * p.hso + 4 * lane) =
             make_uint2(pack2<BF16>(a[0] * inv, a[1] * inv), pack2<BF16>(a[2] * inv, a[3] * inv));
-    if (lane == 0 && p.lse) p.lse[row] = nan ? NAN : sum > 0.0f ? top + logf(sum) : -INFINITY;
+    if (lane == 0 && p.lse) p.lse[tok * p.heads + head] = nan ? NAN : sum > 0.0f ? top + logf(sum) : -INFINITY;
+    }
 }
 
 }  // namespace w4t

@@ -611,6 +611,21 @@ static w4_status gemm_impl(const void* X, w4_dtype act_dtype, int64_t M, int64_t
     if (dev < 0 || dev >= kMaxDevices) return W4_ERR_CUDA;
     cudaStream_t strm = as_stream(stream);
 
+    if (!prefill && !gidx && group_size == 32 && zeros && M > 32) {
+        // A stage of eight token tiles with the scale and zero-point rows of sixteen groups does
+        // not fit shared memory twice: two products of at most 32 rows, one after the other.
+        const size_t ldy = epi ? (size_t)epi->ldy : (size_t)N;
+        w4e::Epilogue rest = epi ? *epi : w4e::Epilogue{};
+        if (rest.residual)
+            rest.residual = reinterpret_cast<const unsigned char*>(rest.residual) + 32 * (size_t)rest.ldr * (rest.res_dtype == W4_F32 ? 4 : 2);
+        st = gemm_impl(X, act_dtype, 32, N, K, qweight, scales, zeros, g_idx, perm, group_size, s_inv, Y, out_dtype,
+                       workspace, workspace_bytes, stream, epi);
+        if (st != W4_OK) return st;
+        return gemm_impl(reinterpret_cast<const unsigned char*>(X) + 32 * (size_t)K * 2, act_dtype, M - 32, N, K, qweight,
+                         scales, zeros, g_idx, perm, group_size, s_inv,
+                         reinterpret_cast<unsigned char*>(Y) + 32 * ldy * dtype_bytes(out_dtype), out_dtype, workspace,
+                         workspace_bytes, stream, epi ? &rest : nullptr);
+    }
     if (!prefill) {
         w4d::DecodeParams p;
         std::memset(&p, 0, sizeof(p));
@@ -1572,7 +1587,7 @@ w4_status launch_attention(const CUtensorMap (&maps)[4], const w4t::AttnParams& 
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, k, maps[0], maps[1], maps[2], maps[3], p) != cudaSuccess) return W4_ERR_CUDA;
     if (p.part_o) {
-        cfg.gridDim = dim3((unsigned)(((size_t)p.total_q * p.heads + 7) / 8));
+        cfg.gridDim = dim3((unsigned)p.ctas, (unsigned)(w4t::kRows / w4t::kJoinRows));
         cfg.blockDim = dim3(256);
         cfg.dynamicSmemBytes = 0;
         if (cudaLaunchKernelEx(&cfg, w4t::combine_kernel<BF16>, p) != cudaSuccess) return W4_ERR_CUDA;

@@ -172,6 +172,23 @@ def test_groups(M, symmetric, group, K):
         run(L, M, residual=dtype)
 
 
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("M", [33, 47, 64])
+def test_small_groups_with_zero_points_between_33_and_64_rows(M, dtype):
+    """Where one stage would not fit shared memory twice the rows are done in two parts; the
+    plain product the same."""
+    skip_without_gpu()
+    torch = torch_mod()
+    L = Layer(13, 144, 576, 32, dtype=dtype)
+    run(L, M, bias=dtype, activation="silu", residual="float32")
+    run(L, M, activation="gelu", gated=True, residual=dtype, s_inv=True)
+    X = L.acts(M)
+    Y = w4.w4a16_gemm(X, L.qw, L.sc, L.zr, 32, out_dtype=torch.float32)
+    y, e = reference(L, X)
+    biased = (L.K / 8 + L.K / 32 + 16) * 2.0 ** -23 * (X.double().abs() @ (L.bound + 1024 * L.sc.double().repeat_interleave(32, 0).t()).t())
+    assert ((Y.double() - y).abs() <= e + 16 * biased).all()   # (the plain product's fp16 codes are biased by 1024, rows r + 8 by 64 of 16 q)
+
+
 @pytest.mark.parametrize("perm", [False, True])
 @pytest.mark.parametrize("M", [1, 20, 80])
 def test_act_order(M, perm):
