@@ -33,7 +33,9 @@
 // of the loop's latency.  Handing P on by halves takes a quarter of P V out of that latency
 // (8192 tokens, 32/8 heads: 461 -> 447 us).  Tried and slower: half-size S tiles, two a
 // tile (540 us: a 128 x 64 product costs as much as a 128 x 128 one), and an eighth, a quarter
-// or a third of the exponentials as a polynomial on the FMA units (456, 467, 472 us).
+// or a third of the exponentials as a polynomial on the FMA units (456, 467, 472 us); a fourth
+// warpgroup for the output beside softmax warps of 184 registers (457 us, and packed prompts
+// 187 against 173).
 //
 // Two ways to share the work:
 //   items    longest first, one CTA an item; a running CTA takes the place of one that has
@@ -1046,11 +1048,59 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int k = 0; k < 8; ++k) to_row[k] = __shfl_sync(0xffffffffu, (unsigned long long)at, 4 * k + (lane >> 3));
             }
+            auto make_room = [&] {
+                if (lane == 0) tma_store_read();   // the last store has read its bytes
+                __syncwarp();
+            };
+            auto send = [&](int c0) {   // the staged columns from c0 on
+                if (whole) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) tma_store_3d(&tmap_o, st, c0, ws->hk * p.group, (int)tok);
+                    return;
+                }
+                __syncwarp();
+                const int col = c0 + (part ? 4 : 8) * (lane & 7);
+                uint4 d[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    d[k] = *reinterpret_cast<const uint4*>(st + (4 * k + (lane >> 3)) * 128 +
+                                                           (((lane & 7) ^ ((4 * k + (lane >> 3)) & 7)) << 4));
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    if (!((live >> (4 * k + (lane >> 3))) & 1u) || col >= p.dim) continue;
+                    if (part) *reinterpret_cast<uint4*>(p.part_o + to_row[k] + col) = d[k];
+                    else *reinterpret_cast<uint4*>(reinterpret_cast<unsigned short*>(p.O) + to_row[k] + col) = d[k];
+                }
+                __syncwarp();
+            };
+            if (pair && !part && n > 0 && ws->poison == 0) {
+                // the common case, O's columns all at once (8 prompts of 1024 tokens, 32/8 heads:
+                // 113 -> 106 us against 32 columns at a time)
+                uint32_t o[DP / 16][16];
+#pragma unroll
+                for (int c = 0; c < DP / 16; ++c) tmem_ld16_async(to + 16 * c, o[c]);
+                tmem_wait_ld();
+#pragma unroll
+                for (int c0 = 0; c0 < DP; c0 += 64) {
+                    if (c0 >= p.dim) break;
+                    make_room();
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const uint32_t* v = &o[(c0 + 8 * q) / 16][(8 * q) % 16];
+                        uint32_t e[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            e[k] = pack2<BF16>(__uint_as_float(v[2 * k]) * own, __uint_as_float(v[2 * k + 1]) * own);
+                        *reinterpret_cast<uint4*>(st + lane * 128 + ((q ^ (lane & 7)) << 4)) = make_uint4(e[0], e[1], e[2], e[3]);
+                    }
+                    send(c0);
+                }
+            } else {
 #pragma unroll 1
             for (int c0 = 0; c0 < p.dim; c0 += cols) {
                 if (!pair && (c0 / cols & 1) != x) continue;   // one tile: the two warps of a row take turns
-                if (lane == 0) tma_store_read();   // the last store has read its bytes
-                __syncwarp();
+                make_room();
                 uint32_t o[2][16];
                 if (part) {
                     load_o(c0, o);
@@ -1082,26 +1132,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                          (size_t)ws->hk * p.hsv, p.ldv, last - first);
                     __syncwarp();
                 }
-                if (whole) {
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) tma_store_3d(&tmap_o, st, c0, ws->hk * p.group, (int)tok);
-                    continue;
-                }
-                __syncwarp();
-                const int col = c0 + (part ? 4 : 8) * (lane & 7);
-                uint4 d[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    d[k] = *reinterpret_cast<const uint4*>(st + (4 * k + (lane >> 3)) * 128 +
-                                                           (((lane & 7) ^ ((4 * k + (lane >> 3)) & 7)) << 4));
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    if (!((live >> (4 * k + (lane >> 3))) & 1u) || col >= p.dim) continue;
-                    if (part) *reinterpret_cast<uint4*>(p.part_o + to_row[k] + col) = d[k];
-                    else *reinterpret_cast<uint4*>(reinterpret_cast<unsigned short*>(p.O) + to_row[k] + col) = d[k];
-                }
-                __syncwarp();
+                send(c0);
+            }
             }
             const float v = l == 0.0f ? -INFINITY : m * p.scale + (logf(l) - kShift * 0.69314718055994531f);
             if (r.live && (pair || x == 0)) {
