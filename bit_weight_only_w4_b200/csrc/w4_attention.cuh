@@ -189,7 +189,8 @@ struct Seqs {
 // f(v) > idx >= f(v + 1), f(v) = sum_b max(0, items of b - v), found by bisection.
 struct Finder {
     Seqs seqs;       // the first 32
-    int mine, top;   // items of this lane's first sequence, the most of any sequence
+    int mine;        // items of this lane's first sequence
+    int top, total;  // the most items of any sequence, all items
     W4_DEV static int items_of(const AttnParams& p, int b) {
         int s, n;
         bool bad = false;
@@ -199,8 +200,14 @@ struct Finder {
     W4_DEV void start(const AttnParams& p, int lane) {
         seqs.load(p, lane);
         int most = mine = (seqs.nq + item_tokens(p) - 1) / item_tokens(p);
-        for (int b = lane + 32; b < p.batch; b += 32) most = max(most, items_of(p, b));
+        total = mine;
+        for (int b = lane + 32; b < p.batch; b += 32) {
+            const int n = items_of(p, b);
+            most = max(most, n);
+            total += n;
+        }
         top = __reduce_max_sync(0xffffffffu, most);
+        total = __reduce_add_sync(0xffffffffu, total);
     }
     W4_DEV int count(const AttnParams& p, int level, int lane) const {
         int c = max(0, mine - level);
@@ -210,14 +217,14 @@ struct Finder {
     W4_DEV Work find(const AttnParams& p, int item, int lane) const {
         Work w = {};
         const int idx = item / p.kv_heads;
-        if (count(p, 0, lane) <= idx) return w;
+        if (total <= idx) return w;
         int lo = 0, hi = top;   // f(lo) > idx >= f(hi)
         while (hi - lo > 1) {
             const int mid = lo + (hi - lo) / 2;
             if (count(p, mid, lane) > idx) lo = mid;
             else hi = mid;
         }
-        int rank = idx - count(p, lo + 1, lane);   // among the sequences with more than lo items
+        int rank = idx - (hi < top ? count(p, hi, lane) : 0);   // among the sequences with more than lo items
         Seqs at = seqs;
         for (int b0 = 0; b0 < p.batch; b0 += 32) {
             if (b0 > 0) at.load(p, b0 + lane);

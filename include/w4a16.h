@@ -77,7 +77,7 @@ typedef enum {
     W4_ERR_UNSUPPORTED = 2, /* legal but not tiled: see the shape rules above          */
     W4_ERR_CUDA = 3,        /* a CUDA call or kernel launch failed                      */
     W4_ERR_TIMEOUT = 4,     /* a kernel gave up a bounded wait (device error word)      */
-    W4_ERR_DEVICE_ARG = 5   /* a kernel found an out-of-range g_idx entry               */
+    W4_ERR_DEVICE_ARG = 5   /* a kernel found an out-of-range g_idx entry or bound      */
 } w4_status;
 
 typedef enum { W4_F16 = 0, W4_BF16 = 1, W4_F32 = 2 } w4_dtype;
@@ -547,8 +547,8 @@ w4_status w4_unpack_canonical(const uint32_t* qweight, int64_t N, int64_t K,
 
 /* Synchronises the current device, then reports and clears the device-side error word:
  * W4_ERR_TIMEOUT if a kernel gave up a bounded wait, W4_ERR_DEVICE_ARG if a kernel met
- * an out-of-range g_idx or permutation entry or an MXFP4 block scale the prefill kernel
- * cannot decode exactly, W4_ERR_CUDA if the device reports a CUDA error, W4_OK.
+ * an out-of-range g_idx or permutation entry, an MXFP4 block scale the prefill kernel
+ * cannot decode exactly or sequence bounds outside their tensors, W4_ERR_CUDA if the device reports a CUDA error, W4_OK.
  * On W4_ERR_TIMEOUT it also zeroes the current device's w4a16_gemm_noalloc scratch again
  * (a timed-out kernel may have left split-K flags in it); workspaces passed to
  * w4a16_gemm belong to the caller, who zeroes them again. */

@@ -100,6 +100,8 @@ CASES = [
     # more than 32 prompts, longest first; one and two tiles an item
     ([(37 * i) % 190 for i in range(45)], None, 4, 2, 64),
     ([300] * 34, None, 8, 2, 128),
+    ([1 + i % 3 for i in range(150)], None, 2, 1, 64),          # one item a sequence
+    ([1] * 100, [200 + 3 * i for i in range(100)], 4, 2, 64),   # ranges over more than 32 sequences
     ([5], [2], 1, 1, 16),
 ]
 
