@@ -35,7 +35,7 @@
 // tile (540 us: a 128 x 64 product costs as much as a 128 x 128 one), and an eighth, a quarter
 // or a third of the exponentials as a polynomial on the FMA units (456, 467, 472 us); a fourth
 // warpgroup for the output beside softmax warps of 184 registers (457 us, and packed prompts
-// 187 against 173).
+// 187 against 173).  As it stands: 437 us, 1258 TFLOP/s.
 //
 // Two ways to share the work:
 //   items    longest first, one CTA an item; a running CTA takes the place of one that has

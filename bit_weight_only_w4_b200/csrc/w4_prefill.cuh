@@ -267,7 +267,7 @@ W4_DEV void load_staged8(const float* src, float (&v)[8]) {
 // over it; the next block's is on its way meanwhile (two areas of kYChunk tokens of each
 // half), the first block's from the tile's start on.  Against fp32 staging with the residual
 // read on the way out: GELU, 1037 x 11008 x 4096, 172 -> 153 us; residual, 2048 x 4096 x
-// 14336, 326 -> 298 us.  Gated outputs stay with fp32 staging: exchanging gate and up between
+// 14336, 320 -> 292 us.  Gated outputs stay with fp32 staging: exchanging gate and up between
 // lanes to halve what is staged took longer (2048 x 28672 x 4096: 583 us against 567).
 struct Drain16 {
     static constexpr int kBlocks = BM / 2 / kYChunk;
@@ -761,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // The same product with an epilogue (kernels of their own: the plain product keeps its code).
 // 2048 x 28672 x 4096 with SwiGLU 567 us (the product alone 536), 2048 x 4096 x 14336 with a
-// residual 297 us (281): the drain's excess over what the two tensor-memory buffers hide.
+// residual 292 us (281): the drain's excess over what the two tensor-memory buffers hide.
 template <bool BF16, int WM, int EPI>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_epi_kernel(const __grid_constant__ CUtensorMap tmap_x, const PrefillParams p, const w4e::Epilogue epi) {
