@@ -875,7 +875,6 @@ def our_arm(args, world, rank, local):
         extras["fp4"] = time_fp4(w4, torch)
         extras["quantize_pack"] = time_quantize(w4, torch, projs)
         extras["awq_search"] = time_awq_search(w4, torch)
-        # last: its larger workspace may replace the cached one the graphs above captured
         extras["actorder_decode"] = time_actorder(w4, torch)
     cpu = None
     if rank == 0 and world == 1 and not args.no_cpu:

@@ -11,6 +11,7 @@ is missing or a call fails, an exception is raised.
     qweight, scales, zeros = w4_quantize_pack(W, s, group_size=128)
     Y = w4a16_gemm(X, qweight, scales, zeros, group_size=128, s_inv=s_inv)
 """
+import contextlib
 import ctypes
 import os
 import struct
@@ -70,6 +71,8 @@ def lib():
         L.w4_unpack_canonical.restype = st
         L.w4_check_device_error.argtypes = []
         L.w4_check_device_error.restype = st
+        L.w4_stream_capture_id.argtypes = [vp, ctypes.POINTER(u64)]
+        L.w4_stream_capture_id.restype = st
         L.w4_set_wait_limit_ns.argtypes = [u64]
         L.w4_set_wait_limit_ns.restype = st
         L.w4_selftest_noalloc_scratch.argtypes = [i32, ctypes.POINTER(u64)]
@@ -194,6 +197,16 @@ def _on_device(index, fn, *args):
         return fn(*args)
     with torch.cuda.device(index):
         return fn(*args)
+
+
+def _allocating_on(stream, device):
+    """Context in which tensors come from the pool of `stream` (None: of the current stream)."""
+    if stream is None:
+        return contextlib.nullcontext()
+    torch = _torch()
+    if not isinstance(stream, torch.cuda.Stream):   # any object with a cuda_stream handle
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+    return torch.cuda.stream(stream)
 
 
 def _check(status, what):
@@ -367,21 +380,54 @@ def w4_quantize_pack(W, s=None, group_size=128, symmetric=False, g_idx=None,
     return qweight, scales, zeros
 
 
-_ws_cache = {}
+_ws_cache = {}      # (device index, stream handle): the buffer of eager calls on that stream
+_ws_captured = {}   # (device index, stream handle): (capture, the buffer of the calls it recorded)
 _ws_lock = threading.Lock()
 
 
-def workspace_for(device, nbytes):
-    """A zero-initialised scratch buffer of at least nbytes on `device`, shared by every
-    call on that device that passes no workspace of its own (the kernels leave it
-    zero-filled where that matters).  Calls sharing it must be ordered on the GPU."""
+def _capture_id(index, handle, stream):
+    """The number of the capture that records the stream's work, 0 while none does."""
     torch = _torch()
-    key = torch.device(device).index
+    if stream is None and torch._C._cuda_getDevice() == index and not torch._C._cuda_isCurrentStreamCapturing():
+        return 0
+    out = ctypes.c_uint64()
+    _check(_on_device(index, lib().w4_stream_capture_id, handle, ctypes.byref(out)), "w4_stream_capture_id")
+    return out.value
+
+
+def workspace_for(device, nbytes, stream=None):
+    """A scratch buffer of at least nbytes on `device`, zero-filled where the kernels want it
+    so, for a call on `stream` (default: the current one) that passes no workspace of its own.
+
+    Calls on one stream share a buffer: they follow one another on the GPU, also where it is
+    outgrown and its memory goes back to that stream's pool.  Calls that a graph capture
+    records share one that belongs to the graph (allocated within the capture, its split-K slots
+    zeroed by every replay), and no later call takes that one.  So graphs may be replayed beside
+    each other and beside eager calls."""
+    torch = _torch()
+    device = torch.device(device)
+    index = torch.cuda.current_device() if device.index is None else device.index
+    handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    capture = _capture_id(index, handle, stream)
+    key = (index, handle)
     with _ws_lock:
-        buf = _ws_cache.get(key)
-        if buf is None or buf.numel() < nbytes:
-            buf = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
-            _ws_cache[key] = buf
+        if capture:
+            owner, buf = _ws_captured.get(key, (0, None))
+            if owner != capture:
+                buf = None
+        else:
+            buf = _ws_cache.get(key)
+        if buf is not None and buf.numel() >= nbytes:
+            return buf
+        nbytes = max(nbytes, 1 << 20)
+        with _allocating_on(stream, device):
+            if capture:
+                # only the slots have to be zero (the activations behind them may be large)
+                buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+                buf[:_workspace_size(index, lib().w4a16_workspace_bytes, 1, 16, 64, 64) or nbytes].zero_()
+                _ws_captured[key] = (capture, buf)
+            else:
+                _ws_cache[key] = buf = torch.zeros(nbytes, dtype=torch.uint8, device=device)
         return buf
 
 
@@ -442,10 +488,10 @@ def w4a16_gemm(X, qweight, scales, zeros, group_size=128, g_idx=None, s_inv=None
     With perm, the weights were packed with that permutation (w4_quantize_pack(perm=...))
     and the activation columns are gathered through it (w4a16_gemm_perm).
 
-    Without `workspace`, every call on a device shares one cached zero-filled buffer, which
-    is safe for calls ordered on one stream.  Calls that may run concurrently (unordered
-    streams) must each pass a workspace of their own: torch.zeros(w4a16_workspace_bytes(...),
-    dtype=torch.uint8, device=...)."""
+    Without `workspace`, the calls on a stream share one cached zero-filled buffer, and those
+    of a graph capture one that belongs to the graph (workspace_for).  A workspace of the
+    caller's, torch.zeros(w4a16_workspace_bytes(...), dtype=torch.uint8, device=...), must not be
+    shared by calls that may run at once (unordered streams, graphs replayed beside others)."""
     torch = _torch()
     M, K, N = _gemm_args(X, qweight, scales, zeros, group_size, g_idx, s_inv, Y, perm)
     if perm is not None and g_idx is not None:
@@ -460,7 +506,7 @@ def w4a16_gemm(X, qweight, scales, zeros, group_size=128, g_idx=None, s_inv=None
         else:
             need = w4a16_workspace_bytes(M, N, K, group_size) if M > 0 else 0
         if workspace is None and need > 0:
-            workspace = workspace_for(dev, need)
+            workspace = workspace_for(dev, need, stream)
         ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
         if perm is not None:
             st = lib().w4a16_gemm_perm(_ptr(X), _dtype_code(X.dtype), M, N, K, _ptr(qweight), _ptr(scales),
@@ -562,7 +608,7 @@ def w4a16_fp4_gemm(X, qweight, block_scales, tensor_scale=None, fmt="nvfp4", out
     with _DeviceGuard(dev):
         need = w4a16_fp4_workspace_bytes(M, N, K, f) if M > 0 else 0
         if workspace is None and need > 0:
-            workspace = workspace_for(dev, need)
+            workspace = workspace_for(dev, need, stream)
         ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
         st = lib().w4a16_fp4_gemm(_ptr(X), _dtype_code(X.dtype), M, N, K, _ptr(qweight), _ptr(block_scales),
                                   _ptr(tensor_scale), f, _ptr(Y), _dtype_code(Y.dtype), _ptr(workspace),
@@ -618,7 +664,7 @@ def w4a16_gemm_chain(layers, workspace=None, stream=None):
     with _DeviceGuard(dev):
         need = w4a16_chain_workspace_bytes(M)
         if workspace is None and need > 0:
-            workspace = workspace_for(dev, need)
+            workspace = workspace_for(dev, need, stream)
         ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
         st = lib().w4a16_gemm_chain(arr, n, M, _dtype_code(act), _dtype_code(out), _ptr(workspace),
                                     ws_bytes, _stream_handle(stream, dev))
@@ -643,16 +689,16 @@ def w4_unpack_canonical(qweight, N, K, out=None, stream=None):
 def w4_check_device_error():
     """Synchronise the current device and raise if a kernel reported an error.  After a
     timeout the library zeroes its allocation-free scratch again, and this binding zeroes
-    its cached workspace of the current device (a kernel that gave up a wait may have left
-    split-K flags in either)."""
+    its cached workspaces of the current device (a kernel that gave up a wait may have left
+    split-K flags in either; the workspaces of graphs are zeroed by every replay)."""
     st = lib().w4_check_device_error()
     if st == W4_ERR_TIMEOUT:
         torch = _torch()
         with _ws_lock:
-            buf = _ws_cache.get(torch.cuda.current_device())
-            if buf is not None:
-                buf.zero_()
-                torch.cuda.synchronize()
+            for (index, _), buf in _ws_cache.items():
+                if index == torch.cuda.current_device():
+                    buf.zero_()
+            torch.cuda.synchronize()
     _check(st, "w4_check_device_error")
 
 
@@ -737,7 +783,7 @@ def w4a16_gemm_epi(X, qweight, scales, zeros, group_size=128, bias=None, activat
         need = _workspace_size(index, L.w4a16_workspace_bytes if perm is None else L.w4a16_workspace_bytes_perm,
                                M, N, K, group_size)
         if need > 0:
-            workspace = workspace_for(X.device, need)
+            workspace = workspace_for(X.device, need, stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     st = _on_device(index, L.w4a16_gemm_epi, X.data_ptr(), _dtype_code(xt), M, N, K, qweight.data_ptr(),
                     scales.data_ptr(), _ptr(zeros), _ptr(g_idx), _ptr(perm), group_size, _ptr(s_inv), e, Y.data_ptr(),

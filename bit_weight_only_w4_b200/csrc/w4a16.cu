@@ -889,6 +889,17 @@ w4_status w4_set_wait_limit_ns(uint64_t ns) {
     return cudaMemcpyToSymbol(g_w4_wait_limit_ns, &v, sizeof(v)) == cudaSuccess ? W4_OK : W4_ERR_CUDA;
 }
 
+w4_status w4_stream_capture_id(w4_stream_t stream, uint64_t* id) {
+    if (!id) return W4_ERR_INVALID_ARG;
+    *id = 0;
+    if (!stream) return W4_OK;
+    cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+    unsigned long long v = 0;
+    if (cudaStreamGetCaptureInfo(as_stream(stream), &status, &v) != cudaSuccess) return W4_ERR_CUDA;
+    if (status == cudaStreamCaptureStatusActive) *id = v;
+    return W4_OK;
+}
+
 }  // extern "C"
 
 namespace {

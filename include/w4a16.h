@@ -554,6 +554,12 @@ w4_status w4_unpack_canonical(const uint32_t* qweight, int64_t N, int64_t K,
  * w4a16_gemm belong to the caller, who zeroes them again. */
 w4_status w4_check_device_error(void);
 
+/* *id = a number, unique in the process, of the graph capture that records the work put on
+ * `stream`, or 0 while none does (the legacy default stream is never captured).  A workspace
+ * that is passed to captured calls must belong to their graph alone: its replays may run beside
+ * calls on any stream. */
+w4_status w4_stream_capture_id(w4_stream_t stream, uint64_t* id);
+
 /* Bound, in nanoseconds, of every wait inside the library's kernels (default 2e9).
  * Lowering it is a test aid; values below 1000 are raised to 1000. */
 w4_status w4_set_wait_limit_ns(uint64_t ns);
