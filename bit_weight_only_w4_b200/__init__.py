@@ -10,6 +10,10 @@ is missing or a call fails, an exception is raised.
 
     qweight, scales, zeros = w4_quantize_pack(W, s, group_size=128)
     Y = w4a16_gemm(X, qweight, scales, zeros, group_size=128, s_inv=s_inv)
+
+Calls run on the current stream, or on the one passed as ``stream``.  What they allocate comes
+from that stream's pool, as under ``torch.cuda.stream(stream)``; their inputs have to be ready
+on it.
 """
 import contextlib
 import ctypes
@@ -209,6 +213,18 @@ def _allocating_on(stream, device):
     return torch.cuda.stream(stream)
 
 
+def _new(like, shape, dtype, stream):
+    """An uninitialised output on `like`'s device of a call on `stream`: from that stream's
+    pool, whose memory no work queued on another stream still reads or writes.  The current
+    stream, where the caller will read it, keeps it until its work is done."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with _allocating_on(stream, like.device):
+        t = like.new_empty(shape, dtype=dtype)
+    t.record_stream(_torch().cuda.current_stream(like.device))
+    return t
+
+
 def _check(status, what):
     if status != W4_OK:
         raise W4Error(status, what)
@@ -302,7 +318,7 @@ def w4_actorder_perm(g_idx, group_size, perm=None, stream=None):
     _expect(perm, "perm", (torch.int32,), numel=K)
     dev = _need_cuda(g_idx, perm)
     if perm is None:
-        perm = torch.empty(K, dtype=torch.int32, device=dev)
+        perm = _new(g_idx, K, torch.int32, stream)
     with _DeviceGuard(dev):
         st = lib().w4_actorder_perm(_ptr(g_idx), K, int(group_size), _ptr(perm), _stream_handle(stream, dev))
     _check(st, "w4_actorder_perm")
@@ -322,7 +338,7 @@ def w4_awq_search(W, X, group_size=128, symmetric=False, n_grid=20, stream=None)
     _expect(W, "W", _f16s())
     _expect(X, "X", _f16s())
     dev = _need_cuda(W, X)
-    s_best = torch.empty(K, dtype=torch.float32, device=dev)
+    s_best = _new(W, K, torch.float32, stream)
     losses = (ctypes.c_double * int(n_grid))()
     best = ctypes.c_int32(-1)
     with _DeviceGuard(dev):
@@ -331,7 +347,8 @@ def w4_awq_search(W, X, group_size=128, symmetric=False, n_grid=20, stream=None)
             raise ValueError("w4_awq_search: unsupported sizes")
         # a buffer of its own: the search writes over the front of its workspace, where the
         # cached GEMM workspace keeps the zero-filled split-K slots
-        ws = torch.zeros(need, dtype=torch.uint8, device=dev)
+        with _allocating_on(stream, dev):
+            ws = torch.zeros(need, dtype=torch.uint8, device=dev)
         st = lib().w4_awq_search(_ptr(W), _dtype_code(W.dtype), N, K, _ptr(X), _dtype_code(X.dtype), M,
                                  int(group_size), int(bool(symmetric)), int(n_grid), _ptr(s_best),
                                  ctypes.addressof(losses), ctypes.addressof(best), _ptr(ws),
@@ -362,11 +379,11 @@ def w4_quantize_pack(W, s=None, group_size=128, symmetric=False, g_idx=None,
     _expect(zeros, "zeros", (torch.float16,), shape=(G, N))
     dev = _need_cuda(W, s, g_idx, qweight, scales, zeros, perm)
     if qweight is None:
-        qweight = torch.empty(N * K // 8, dtype=torch.int32, device=dev)
+        qweight = _new(W, N * K // 8, torch.int32, stream)
     if scales is None:
-        scales = torch.empty(G, N, dtype=torch.float16, device=dev)
+        scales = _new(W, (G, N), torch.float16, stream)
     if zeros is None and not symmetric:
-        zeros = torch.empty(G, N, dtype=torch.float16, device=dev)
+        zeros = _new(W, (G, N), torch.float16, stream)
     with _DeviceGuard(dev):
         if perm is not None:
             st = lib().w4_quantize_pack_perm(_ptr(W), _dtype_code(W.dtype), N, K, _ptr(s), int(group_size),
@@ -499,7 +516,7 @@ def w4a16_gemm(X, qweight, scales, zeros, group_size=128, g_idx=None, s_inv=None
     dev = _need_cuda(X, qweight, scales, zeros, g_idx, s_inv, Y, workspace, perm)
     out_dtype = out_dtype or X.dtype
     if Y is None:
-        Y = torch.empty(M, N, dtype=out_dtype, device=dev)
+        Y = _new(X, (M, N), out_dtype, stream)
     with _DeviceGuard(dev):
         if perm is not None:
             need = lib().w4a16_workspace_bytes_perm(M, N, K, int(group_size)) if M > 0 else 0
@@ -532,7 +549,7 @@ def w4a16_gemm_noalloc(X, qweight, scales, zeros, group_size=128, g_idx=None, s_
     dev = _need_cuda(X, qweight, scales, zeros, g_idx, s_inv, Y)
     out_dtype = out_dtype or X.dtype
     if Y is None:
-        Y = torch.empty(M, N, dtype=out_dtype, device=dev)
+        Y = _new(X, (M, N), out_dtype, stream)
     with _DeviceGuard(dev):
         st = lib().w4a16_gemm_noalloc(_ptr(X), _dtype_code(X.dtype), M, N, K, _ptr(qweight),
                                       _ptr(scales), _ptr(zeros), _ptr(g_idx), int(group_size),
@@ -567,11 +584,11 @@ def w4_fp4_quantize_pack(W, fmt="nvfp4", qweight=None, block_scales=None, tensor
     _expect(tensor_scale, "tensor_scale", (torch.float32,), numel=1)
     dev = _need_cuda(W, qweight, block_scales, tensor_scale)
     if qweight is None:
-        qweight = torch.empty(N * K // 8, dtype=torch.int32, device=dev)
+        qweight = _new(W, N * K // 8, torch.int32, stream)
     if block_scales is None:
-        block_scales = torch.empty(K // B, N, dtype=torch.uint8, device=dev)
+        block_scales = _new(W, (K // B, N), torch.uint8, stream)
     if f == W4_FP4_NVFP4 and tensor_scale is None:
-        tensor_scale = torch.empty(1, dtype=torch.float32, device=dev)
+        tensor_scale = _new(W, 1, torch.float32, stream)
     if f == W4_FP4_MXFP4:
         tensor_scale = None
     with _DeviceGuard(dev):
@@ -604,7 +621,7 @@ def w4a16_fp4_gemm(X, qweight, block_scales, tensor_scale=None, fmt="nvfp4", out
     dev = _need_cuda(X, qweight, block_scales, tensor_scale, Y, workspace)
     out_dtype = out_dtype or (Y.dtype if Y is not None else X.dtype)
     if Y is None:
-        Y = torch.empty(M, N, dtype=out_dtype, device=dev)
+        Y = _new(X, (M, N), out_dtype, stream)
     with _DeviceGuard(dev):
         need = w4a16_fp4_workspace_bytes(M, N, K, f) if M > 0 else 0
         if workspace is None and need > 0:
@@ -678,7 +695,7 @@ def w4_unpack_canonical(qweight, N, K, out=None, stream=None):
     _expect(out, "out", _words(), numel=N * K // 8)
     dev = _need_cuda(qweight, out)
     if out is None:
-        out = torch.empty(N, K // 8, dtype=torch.int32, device=dev)
+        out = _new(qweight, (N, K // 8), torch.int32, stream)
     with _DeviceGuard(dev):
         st = lib().w4_unpack_canonical(_ptr(qweight), int(N), int(K), _ptr(out),
                                        _stream_handle(stream, dev))
@@ -766,7 +783,7 @@ def w4a16_gemm_epi(X, qweight, scales, zeros, group_size=128, bias=None, activat
     xt = X.dtype
     if Y is None:
         yt = out_dtype or xt
-        Y = X.new_empty((M, n_out)) if yt is xt else X.new_empty((M, n_out), dtype=yt)
+        Y = _new(X, (M, n_out), yt, stream)
         ldy = n_out
     else:
         yt = Y.dtype
@@ -855,7 +872,7 @@ def w4_rope(X, positions, inv_freq, interleaved=False, mscale=1.0, Y=None, strea
     xt = X.dtype
     if Y is None:
         index = _cuda_index(X, positions, inv_freq)
-        Y = X.new_empty(shape)
+        Y = _new(X, shape, xt, stream)
         sy = (H * D, D)
     else:
         index = _cuda_index(X, positions, inv_freq, Y)
@@ -913,13 +930,13 @@ def w4_prompt_attention(Q, K, V, cu_seqlens=None, cu_seqlens_k=None, causal=True
                                  "cu_seqlens of the same length")
     index = _cuda_index(Q, K, V, cu_seqlens, cu_seqlens_k, O, workspace)
     if O is None:
-        O = Q.new_empty((Tq, H, D))
+        O = _new(Q, (Tq, H, D), dt, stream)
         so = (H * D, D)
     else:
         os_, so = _heads_of(O, "O")
         if O.dtype is not dt or os_ != (Tq, H, D):
             _expect(O, "O", (dt,), shape=(Tq, H, D))
-    lse = Q.new_empty((Tq, H), dtype=torch.float32) if return_lse else None
+    lse = _new(Q, (Tq, H), torch.float32, stream) if return_lse else None
     # w4_attention, packed at once (a ctypes structure of 24 fields takes longer to fill)
     a = _ATTENTION.pack(Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), 0 if lse is None else lse.data_ptr(),
                         0 if cu_seqlens is None else cu_seqlens.data_ptr(),
@@ -930,12 +947,8 @@ def w4_prompt_attention(Q, K, V, cu_seqlens=None, cu_seqlens_k=None, causal=True
     if workspace is None:
         need = _workspace_size(index, L.w4_prompt_attention_workspace_bytes, batch, H, Hk, D, Tq, Tk)
         if need > 0:
-            # of the stream that uses it, so that its next use is ordered behind this call
-            if stream is None:
+            with _allocating_on(stream, Q.device):   # its next use is ordered behind this call
                 workspace = Q.new_empty(need, dtype=torch.uint8)
-            else:
-                with torch.cuda.stream(stream):
-                    workspace = Q.new_empty(need, dtype=torch.uint8)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     st = _on_device(index, L.w4_prompt_attention, a, _dtype_code(dt), _ptr(workspace), ws_bytes,
                     torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
