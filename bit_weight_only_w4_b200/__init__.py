@@ -929,6 +929,8 @@ def w4_prompt_attention(Q, K, V, cu_seqlens=None, cu_seqlens_k=None, causal=True
                 raise ValueError(f"{name} must be a contiguous vector of batch+1 bounds, cu_seqlens_k with a "
                                  "cu_seqlens of the same length")
     index = _cuda_index(Q, K, V, cu_seqlens, cu_seqlens_k, O, workspace)
+    if workspace is not None and not workspace.is_contiguous():   # (an expanded one holds less than it counts)
+        raise ValueError("workspace must be contiguous")
     if O is None:
         O = _new(Q, (Tq, H, D), dt, stream)
         so = (H * D, D)

@@ -209,6 +209,15 @@ def test_attention_binding_refusals():
         w4.w4_prompt_attention(t[0], t, t)
 
 
+def test_attention_refuses_a_workspace_that_counts_more_than_it_holds(monkeypatch):
+    """An expanded tensor has the bytes asked for by its count and one by its memory."""
+    import torch
+    monkeypatch.setattr(w4, "_cuda_index", lambda *t: 0)
+    t = torch.zeros(4, 2, 64, dtype=torch.float16)
+    with pytest.raises(ValueError, match="contiguous"):
+        w4.w4_prompt_attention(t, t, t, workspace=torch.zeros(1, dtype=torch.uint8).expand(1 << 24))
+
+
 # ---------------------------------------------------------------- build
 def test_new_kernels_do_not_spill(L):
     """The one-, four- and eight-token-tile products with an epilogue and the prompt kernels
