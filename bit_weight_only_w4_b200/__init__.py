@@ -928,6 +928,8 @@ def w4_prompt_attention(Q, K, V, cu_seqlens=None, cu_seqlens_k=None, causal=True
             if cu_seqlens is None or batch < 0 or cu.shape != (batch + 1,) or not cu.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous vector of batch+1 bounds, cu_seqlens_k with a "
                                  "cu_seqlens of the same length")
+    if scale is None:
+        scale = D ** -0.5 if D > 0 else 1.0   # (heads without elements are refused by the library)
     index = _cuda_index(Q, K, V, cu_seqlens, cu_seqlens_k, O, workspace)
     if workspace is not None and not workspace.is_contiguous():   # (an expanded one holds less than it counts)
         raise ValueError("workspace must be contiguous")
@@ -943,7 +945,7 @@ def w4_prompt_attention(Q, K, V, cu_seqlens=None, cu_seqlens_k=None, causal=True
     a = _ATTENTION.pack(Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), 0 if lse is None else lse.data_ptr(),
                         0 if cu_seqlens is None else cu_seqlens.data_ptr(),
                         0 if cu_seqlens_k is None else cu_seqlens_k.data_ptr(), Tq, Tk, sq[0], sq[1], sk[0], sk[1],
-                        sv[0], sv[1], so[0], so[1], batch, H, Hk, D, D ** -0.5 if scale is None else scale,
+                        sv[0], sv[1], so[0], so[1], batch, H, Hk, D, scale,
                         1 if causal else 0)
     L = lib()
     if workspace is None:

@@ -218,6 +218,16 @@ def test_attention_refuses_a_workspace_that_counts_more_than_it_holds(monkeypatc
         w4.w4_prompt_attention(t, t, t, workspace=torch.zeros(1, dtype=torch.uint8).expand(1 << 24))
 
 
+def test_attention_refuses_heads_without_elements(L, monkeypatch):
+    import torch
+    monkeypatch.setattr(w4, "_cuda_index", lambda *t: 0)
+    monkeypatch.setattr(w4, "_on_device", lambda index, fn, *a: fn(*a))
+    t = torch.zeros(4, 2, 0, dtype=torch.float16)
+    with pytest.raises(w4.W4Error) as e:
+        w4.w4_prompt_attention(t, t, t, workspace=torch.zeros(1, dtype=torch.uint8), stream=type("S", (), {"cuda_stream": 0}), O=t)
+    assert e.value.status == w4.W4_ERR_INVALID_ARG
+
+
 # ---------------------------------------------------------------- build
 def test_new_kernels_do_not_spill(L):
     """The one-, four- and eight-token-tile products with an epilogue and the prompt kernels
