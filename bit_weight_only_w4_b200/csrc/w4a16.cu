@@ -1386,6 +1386,24 @@ extern "C" w4_status w4a16_fp4_gemm(const void* X, w4_dtype act_dtype, int64_t M
 // ---------------------------------------------------------------------------------------
 namespace {
 
+// Whether elements of a [tokens, heads, dim] view share a place (strides not negative): two
+// runs of dim elements, dt tokens and dh heads apart, that start less than dim elements
+// from each other.
+bool elements_shared(int64_t tokens, int64_t heads, int64_t dim, int64_t token_stride, int64_t head_stride) {
+    if ((tokens > 1 && token_stride < dim) || (heads > 1 && head_stride < dim)) return true;
+    if (tokens <= 1 || heads <= 1) return false;
+    using Wide = __int128;
+    const Wide ts = token_stride, hs = head_stride;
+    // the usual layouts: all heads of a token before the next token, or the other way round
+    if (ts >= (heads - 1) * hs + dim || hs >= (tokens - 1) * ts + dim) return false;
+    for (int64_t dh = 1; dh < heads; ++dh) {
+        const Wide dt = dh * hs / ts, behind = dh * hs - dt * ts;   // the last token that starts no later
+        if (dt < tokens && behind < dim) return true;
+        if (dt + 1 < tokens && ts - behind < dim) return true;
+    }
+    return false;
+}
+
 template <int DT, int E>
 w4_status launch_rope(w4r::RopeParams p, int sms, cudaStream_t stream) {
     const int half = p.rot / 2;
@@ -1440,7 +1458,7 @@ extern "C" w4_status w4_rope(const void* X, w4_dtype dtype, int64_t tokens, int3
     if (!aligned(X, esz) || !aligned(Y, esz) || !aligned(positions, 4) || !aligned(inv_freq, 8)) return W4_ERR_INVALID_ARG;
     if (x_token_stride < 0 || x_head_stride < 0 || y_token_stride < 0 || y_head_stride < 0) return W4_ERR_INVALID_ARG;
     // outputs that share an element would race
-    if ((tokens > 1 && y_token_stride < head_dim) || (heads > 1 && y_head_stride < head_dim)) return W4_ERR_INVALID_ARG;
+    if (elements_shared(tokens, heads, head_dim, y_token_stride, y_head_stride)) return W4_ERR_INVALID_ARG;
     const bool in_place = X == Y;
     if (in_place && ((tokens > 1 && x_token_stride != y_token_stride) || (heads > 1 && x_head_stride != y_head_stride)))
         return W4_ERR_INVALID_ARG;

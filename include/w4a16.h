@@ -438,8 +438,9 @@ w4_status w4a16_gemm_epi(const void* X, w4_dtype act_dtype, int64_t M, int64_t N
  * The angle is taken in fp64, sine, cosine and the rotation in fp32, rounded once.
  *   X           device; element d of head h of token t is X[t*x_token_stride +
  *               h*x_head_stride + d] (strides in elements); fp16, bf16 or fp32 (dtype)
- *   Y           device, the same type, strides of its own.  Y == X with equal strides rotates
- *               in place; any other overlap is not allowed
+ *   Y           device, the same type, strides of its own that give every element its own
+ *               place (checked).  Y == X with equal strides rotates in place; any other
+ *               overlap is not allowed
  *   positions   device int32 [tokens];  inv_freq  device fp64 [rot_dim/2]
  *   rot_dim     even, 2 .. head_dim;  head_dim at most 512;  mscale finite
  * Any stride and alignment of whole elements works; 16-byte alignment of the pointers and

@@ -100,6 +100,31 @@ def test_rope_refusals(L):
     assert rope_call(L, T=0) == w4.W4_OK and rope_call(L, H=0, X=None, Y=None) == w4.W4_OK
 
 
+def shared_places(T, H, D, st, sh):
+    """Whether two elements of a [T, H, D] view with these strides share a place."""
+    at = (np.arange(T)[:, None, None] * st + np.arange(H)[None, :, None] * sh + np.arange(D)).ravel()
+    return len(np.unique(at)) < at.size
+
+
+def test_rope_refuses_outputs_that_share_elements(L):
+    """Every pair of strides of small views, among them those where each stride alone leaves
+    room for a head; the accepted ones are told by the missing device (this test's pointers are
+    no memory, and accepted calls end at the device query)."""
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("accepted calls would be launched")
+    D = 4
+    for T, H in ((2, 2), (3, 2), (2, 5), (4, 3), (7, 6)):
+        for st in range(0, 40):
+            for sh in range(0, 40):
+                got = rope_call(L, T=T, H=H, D=D, rot=D, sx=(H * D, D), sy=(st, sh))
+                want = w4.W4_ERR_INVALID_ARG if shared_places(T, H, D, st, sh) else w4.W4_ERR_CUDA
+                assert got == want, (T, H, st, sh, got)
+    big = 1 << 61   # products of strides and counts pass 64 bits
+    assert rope_call(L, T=1 << 20, H=1 << 15, sy=(64, big)) == w4.W4_ERR_CUDA
+    assert rope_call(L, T=1 << 20, H=1 << 15, sy=(64, 64 << 19)) == w4.W4_ERR_INVALID_ARG
+
+
 def freqs(rot, theta=10000.0, scaling=0, factor=1.0, context=8192.0, lo=1.0, hi=4.0):
     out, m = (ctypes.c_double * max(1, rot // 2))(), ctypes.c_float()
     st = w4.lib().w4_rope_freqs(rot, theta, scaling, factor, context, lo, hi, out, ctypes.byref(m))
