@@ -1658,6 +1658,8 @@ extern "C" w4_status w4_prompt_attention(const w4_attention* a, w4_dtype dtype, 
         if (strides[i] < a->head_dim || strides[i] % 8 != 0) return W4_ERR_INVALID_ARG;
         if (strides[i] >= (int64_t)1 << 38) return W4_ERR_UNSUPPORTED;   // tensor maps hold 2^40 bytes
     }
+    // outputs that share an element would race
+    if (elements_shared(a->q_tokens, a->heads, a->head_dim, a->o_token_stride, a->o_head_stride)) return W4_ERR_INVALID_ARG;
     const int dev = current_device();
     const int sms = dev >= 0 ? sm_count(dev) : 0;
     if (dev >= kMaxDevices || sms <= 0) return W4_ERR_CUDA;

@@ -495,7 +495,8 @@ w4_status w4_rope_freqs(int32_t rot_dim, double theta, w4_rope_scaling scaling, 
  *   a         HOST descriptor, read during the call only:
  *     Q, K, V, O  device, dtype fp16 or bf16; element d of head h of token t at
  *                 t*token_stride + h*head_stride + d (strides in elements, multiples of 8;
- *                 pointers 16-byte aligned).  O must not overlap Q, K or V
+ *                 pointers 16-byte aligned).  O's strides give every element its own place
+ *                 (checked), and O must not overlap Q, K or V
  *     lse         device fp32 [q_tokens, heads] log of the softmax sum (natural), or NULL
  *     cu_seqlens_q, cu_seqlens_k  device int32 [batch+1], ascending.  cu_seqlens_k NULL: the
  *                 same as cu_seqlens_q; both NULL: one sequence (batch == 1) of all tokens.

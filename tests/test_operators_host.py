@@ -234,6 +234,22 @@ def test_attention_binding_refusals():
         w4.w4_prompt_attention(t[0], t, t)
 
 
+def test_attention_refuses_outputs_that_share_elements(L):
+    """As for the rotary positions; strides are multiples of 8."""
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("accepted calls would be launched")
+    D = 16
+    for T, H in ((2, 2), (3, 2), (2, 5), (4, 3)):
+        for st in range(0, 160, 8):
+            for sh in range(0, 160, 8):
+                got = attn_call(L, q_tokens=T, k_tokens=T, heads=H, kv_heads=H, head_dim=D, q_token_stride=H * D, q_head_stride=D,
+                                k_token_stride=H * D, k_head_stride=D, v_token_stride=H * D, v_head_stride=D,
+                                o_token_stride=st, o_head_stride=sh)
+                want = w4.W4_ERR_INVALID_ARG if shared_places(T, H, D, st, sh) else w4.W4_ERR_CUDA
+                assert got == want, (T, H, st, sh, got)
+
+
 def test_attention_refuses_a_workspace_that_counts_more_than_it_holds(monkeypatch):
     """An expanded tensor has the bytes asked for by its count and one by its memory."""
     import torch
