@@ -1016,6 +1016,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int n_other = pair ? 0 : x ? ws->sub0 : ws->sub1;
             const int head = ws->hk * p.group + (threadIdx.x & (kRows - 1)) - rg * p.group;
             const bool part = ws->part >= 0;
+            // Of the keys that this warp's rows see, every one has been looked at (`fixed`, then the
+            // products, then `o_done`); for later keys other warps may still be setting the mark.  One
+            // read for the whole warp: what follows it is warp-wide.
+            const bool poison = __any_sync(0xffffffffu, ws->poison != 0);
             // row offsets in the output, and where the rows of this warp that are tokens lie
             const size_t tok = (size_t)(ws->q0 + r.tok);
             const size_t prow = (size_t)ws->part * kRows + (threadIdx.x & (kRows - 1));
@@ -1081,7 +1085,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
             };
-            if (pair && !part && n > 0 && ws->poison == 0) {
+            if (pair && !part && n > 0 && !poison) {
                 // the common case, O's columns all at once (8 prompts of 1024 tokens, 32/8 heads:
                 // 113 -> 106 us against 32 columns at a time)
                 uint32_t o[DP / 16][16];
@@ -1132,7 +1136,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
-                if (ws->poison != 0) {
+                if (poison) {
                     const int first = ws->b0 * kKeys + common, last = min(r.limit, ws->b0 * kKeys + (n + n_other) * kSub);
                     repair_row<BF16>(st + lane * 128, lane, part, c0, min(cols, p.dim - c0),
                                      reinterpret_cast<const unsigned short*>(p.V) + (size_t)(ws->k0 + first) * p.ldv +

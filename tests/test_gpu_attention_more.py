@@ -1,0 +1,47 @@
+"""More of prompt attention, with the plain form and the bound of test_gpu_attention.py: non-finite
+values strewn over V."""
+import math
+
+import pytest
+
+import bit_weight_only_w4_b200 as w4
+from tests.gpu_util import skip_without_gpu, torch_mod
+from tests.test_gpu_attention import WAYS, call, way
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("name", WAYS)
+def test_non_finite_values_strewn_over_v(name, dtype):
+    """A row's output is non-finite exactly in the columns where a key that it sees is, with the
+    sign that adding them gives; everywhere else it has the bits it has without them."""
+    skip_without_gpu()
+    torch = torch_mod()
+    w = way(name, dtype=dtype)
+    q, k, Q, K, V, cu_q, cu_k = w
+    clean, lse0 = call(w, return_lse=True)
+    G, Tq = Q.shape[1] // K.shape[1], Q.shape[0]
+    g = torch.Generator(device="cuda").manual_seed(8)
+    V2 = V.clone()
+    keys = torch.randperm(V.shape[0], generator=g, device="cuda")[:max(3, V.shape[0] // 60)]
+    for n, (key, value) in enumerate(zip(keys.tolist(), [math.inf, -math.inf, math.nan] * V.shape[0])):
+        V2[key, n % V.shape[1], (37 * n) % V.shape[2]] = value
+    # what a row sees: running sums of the marks along each sequence
+    marks = torch.stack([V2.isnan(), torch.isposinf(V2), torch.isneginf(V2)]).double()
+    want = clean.float().clone()
+    for b in range(len(q)):
+        a0, b0 = int(cu_q[b]), int(cu_k[b])
+        run = marks[:, b0:b0 + k[b]].cumsum(1)
+        last = torch.arange(q[b], device="cuda") + k[b] - q[b]
+        nan, pos, neg = (r.repeat_interleave(G, 1) > 0 for r in run[:, last])
+        rows = want[a0:a0 + q[b]]
+        rows[pos] = math.inf
+        rows[neg] = -math.inf
+        rows[nan | (pos & neg)] = math.nan
+    for _ in range(4):
+        O, lse = w4.w4_prompt_attention(Q, K, V2, cu_q, None if q is k else cu_k, return_lse=True)
+        assert torch.equal(torch.nan_to_num(O.float(), 1e30, 2e30, -2e30), torch.nan_to_num(want, 1e30, 2e30, -2e30))
+        assert torch.equal(lse, lse0)
+    assert Tq == O.shape[0] and not want.isfinite().all()
+    w4.w4_check_device_error()
