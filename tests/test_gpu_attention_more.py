@@ -1,14 +1,42 @@
-"""More of prompt attention, with the plain form and the bound of test_gpu_attention.py: non-finite
-values strewn over V."""
+"""More of prompt attention, with the plain form and the bound of test_gpu_attention.py: scores of
+hundreds whose error stays small in every way of working, non-finite values strewn over V."""
 import math
 
 import pytest
 
 import bit_weight_only_w4_b200 as w4
 from tests.gpu_util import skip_without_gpu, torch_mod
-from tests.test_gpu_attention import WAYS, call, way
+from tests.test_gpu_attention import WAYS, call, check, make, plain, way
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("shape", ["rising", "falling", "zigzag"])
+@pytest.mark.parametrize("name", WAYS)
+def test_scores_of_hundreds(name, shape, dtype):
+    """Every query has a common part w (signs) and keys have a multiple of it that changes along
+    the sequence, so scores run over 240: rising, falling, or both by turns within a key block.
+    A score's error bound d is then D 2^-23 of about 300, so the check means something: weights
+    are held to 2 d < 0.01."""
+    skip_without_gpu()
+    torch = torch_mod()
+    D, scale = 64, 0.125
+    q, k, H, Hk = WAYS[name]
+    same = k is None
+    k = q if same else k
+    dt = getattr(torch, dtype)
+    Q, K, V, cu_q, cu_k = make(21, q, k, H, Hk, D, dt)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    w = torch.sign(torch.randn(D, generator=g, device="cuda"))
+    at = torch.cat([torch.linspace(0, 1, n, device="cuda") if n > 1 else torch.ones(n, device="cuda") for n in k])
+    step = {"rising": at, "falling": 1 - at, "zigzag": torch.frac(at * 7.3) * at}[shape] * 30
+    Q = (Q.float() + w).to(dt)
+    K = (0.3 * K.float() + step[:, None, None] * w).to(dt)
+    ref = plain(Q, K, V, q, k, True, scale)
+    assert float(ref[1].max()) > 150 and 2 * float(ref[3].max()) < 0.01
+    O, lse = w4.w4_prompt_attention(Q, K, V, cu_q, None if same else cu_k, scale=scale, return_lse=True)
+    check(O, lse, ref, dt, max(k))
 
 
 @pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
