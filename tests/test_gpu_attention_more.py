@@ -1,5 +1,6 @@
 """More of prompt attention, with the plain form and the bound of test_gpu_attention.py: scores of
-hundreds whose error stays small in every way of working, non-finite values strewn over V."""
+hundreds whose error stays small in every way of working, non-finite values strewn over V,
+prompts packed with next tokens, and the same bits every time."""
 import math
 
 import pytest
@@ -73,3 +74,28 @@ def test_non_finite_values_strewn_over_v(name, dtype):
         assert torch.equal(lse, lse0)
     assert Tq == O.shape[0] and not want.isfinite().all()
     w4.w4_check_device_error()
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("q_lens,k_lens", [([300, 1, 1, 1], [300, 2500, 700, 4000]), ([1, 1, 700, 1, 40], [1300, 64, 700, 5000, 3000]),
+                                           ([1] * 20 + [600], [128 * i + 1 for i in range(20)] + [600])])
+def test_prompts_packed_with_next_tokens(q_lens, k_lens, dtype):
+    skip_without_gpu()
+    torch = torch_mod()
+    dt = getattr(torch, dtype)
+    Q, K, V, cu_q, cu_k = make(31, q_lens, k_lens, 16, 2, 128, dt)
+    O, lse = w4.w4_prompt_attention(Q, K, V, cu_q, cu_k, return_lse=True)
+    w4.w4_check_device_error()
+    check(O, lse, plain(Q, K, V, q_lens, k_lens, True, 128 ** -0.5), dt, max(k_lens))
+
+
+@pytest.mark.parametrize("name", WAYS)
+def test_the_same_bits_every_time(name):
+    """No sum's order depends on which CTA or warp comes first."""
+    skip_without_gpu()
+    torch = torch_mod()
+    w, other = way(name), way(name, seed=6)
+    want = call(w, return_lse=True)
+    for _ in range(10):
+        call(other)
+        assert all(torch.equal(a, b) for a, b in zip(call(w, return_lse=True), want))
