@@ -59,7 +59,8 @@ struct Act {
         if constexpr (K == kKindClamp) return x < a ? a : x;
         else if constexpr (K == kKindErf) return 0.5f * x * erfcf(-0.70710678118654752f * x);
         // for e^-u beyond 2^126 the quotient is below 2^-100: __fdividef's zero there is right
-        else return __fdividef(x, 1.0f + __expf(-x * fmaf(c * x, x, a)));
+        // (fminf: with c = 0 an infinite x makes the argument's factor NaN; activate(inf) is inf)
+        else return __fdividef(x, 1.0f + __expf(-x * fminf(fmaf(c * x, x, a), 3.0e38f)));
     }
 };
 W4_DEV float activate(const Act& act, float x) {
