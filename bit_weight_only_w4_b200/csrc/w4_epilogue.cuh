@@ -33,14 +33,19 @@ W4_DEV float load_elem(const void* p, int dtype, size_t i) {
     return __half2float(reinterpret_cast<const __half*>(p)[i]);
 }
 
-// One fp32 activation.  The exponential is the hardware's 2^x (a few ulp of fp32 over the
-// range where the result is not negligible): far below the rounding to a 16-bit Y.
+// One fp32 activation.
 //   none, relu  x, not below `low` (-inf, 0; NaN stays NaN)
 //   silu        x / (1 + e^-x)
 //   gelu_tanh   x/2 (1 + tanh w) = x / (1 + e^-2w),  2w = sqrt(8/pi) (x + 0.044715 x^3): the
-//               same form as silu with another argument
+//               same form as silu with another argument u
 //   gelu        x Phi(x) = x/2 erfc(-x / sqrt 2)      (erfc keeps the negative tail's digits)
-enum : int { kKindClamp = 0, kKindSigmoid = 1, kKindErf = 2 };
+// Two forms of the second kind.  Short: the hardware's 2^x of u log2 e rounded, whose error
+// grows with |u| to 2^-17 of the result, still far below the rounding to a 16-bit Y; for prompts
+// with a 16-bit Y, where every instruction of the drain counts.  Full: what the rounding of
+// u log2 e left out (of the product, by fma, and of the constant) is multiplied back in, so the
+// exponential is within a few ulp for every u; for an fp32 Y, and for decode, where outputs are
+// few.
+enum : int { kKindClamp = 0, kKindSigmoid = 1, kKindErf = 2, kKindSigmoidFull = 3 };
 template <int K>
 struct KindOf {
     static constexpr int value = K;
@@ -60,11 +65,24 @@ struct Act {
         else if constexpr (K == kKindErf) return 0.5f * x * erfcf(-0.70710678118654752f * x);
         // for e^-u beyond 2^126 the quotient is below 2^-100: __fdividef's zero there is right
         // (fminf: with c = 0 an infinite x makes the argument's factor NaN; activate(inf) is inf)
-        else return __fdividef(x, 1.0f + __expf(-x * fminf(fmaf(c * x, x, a), 3.0e38f)));
+        else if constexpr (K == kKindSigmoid)
+            return __fdividef(x, 1.0f + __expf(-x * fminf(fmaf(c * x, x, a), 3.0e38f)));
+        else return __fdividef(x, 1.0f + exp_of_argument(x));
+    }
+    // e^-u, u the argument of x; x beyond 104 either way counts as 104, where e^-u is already
+    // infinite, or nothing beside 1
+    W4_DEV float exp_of_argument(float x) const {
+        constexpr float kLog2e = 1.44269502f, kRest = 1.925963e-8f, kLn2 = 0.693147182f;   // log2 e = kLog2e + kRest
+        const float y = fminf(fmaxf(x, -104.0f), 104.0f);
+        const float v = -y * fmaf(c * y, y, a);
+        const float t = v * kLog2e, rest = fmaf(v, kRest, fmaf(v, kLog2e, -t));
+        float e;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+        return e * fmaf(rest, kLn2, 1.0f);
     }
 };
 W4_DEV float activate(const Act& act, float x) {
-    if (act.kind == kKindSigmoid) return act.apply<kKindSigmoid>(x);
+    if (act.kind == kKindSigmoid) return act.apply<kKindSigmoidFull>(x);
     if (act.kind == kKindErf) return act.apply<kKindErf>(x);
     return act.apply<kKindClamp>(x);
 }

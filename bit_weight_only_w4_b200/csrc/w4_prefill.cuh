@@ -693,9 +693,12 @@ W4_DEV void prefill_body(const CUtensorMap& tmap_x, const PrefillParams& p, cons
                             if (mm >= p.M || pc >= npc) continue;
                             float v[8];
                             load_staged8(ys + m * BN + (epi.gated ? 16 : 8) * pc, v);
-                            if (act.kind == w4e::kKindSigmoid) {
+                            if (act.kind == w4e::kKindSigmoid && p.out_dtype != 2) {
 #pragma unroll
                                 for (int i = 0; i < 8; ++i) v[i] = act.apply<w4e::kKindSigmoid>(v[i]);
+                            } else if (act.kind == w4e::kKindSigmoid) {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) v[i] = act.apply<w4e::kKindSigmoidFull>(v[i]);
                             } else if (act.kind == w4e::kKindClamp) {
 #pragma unroll
                                 for (int i = 0; i < 8; ++i) v[i] = act.apply<w4e::kKindClamp>(v[i]);

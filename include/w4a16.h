@@ -387,7 +387,9 @@ w4_status w4a16_gemm_noalloc(const void* X, w4_dtype act_dtype, int64_t M, int64
  * scales, zeros and bias follow the packed order).
  *
  *   activation  W4_ACT_NONE, W4_ACT_RELU, W4_ACT_SILU x/(1+e^-x), W4_ACT_GELU x Phi(x),
- *               W4_ACT_GELU_TANH x/2 (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3)))
+ *               W4_ACT_GELU_TANH x/2 (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))); in fp32: SiLU
+ *               within 2^-20 of its value, the GELUs within 2^-20 (1 + x^2) of theirs (and
+ *               |x| 2^-126); with 16-bit outputs of M > 64 SiLU within 2^-20 (1 + |x|)
  *   bias        device [N] in packed row order, of bias_dtype (fp16, bf16 or fp32), or NULL
  *   residual    device [M, N_out] of residual_dtype, rows ldr elements apart, or NULL.  It may
  *               be Y itself (same pointer, ldr == ldy, residual_dtype == out_dtype): each

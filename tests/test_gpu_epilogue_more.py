@@ -45,3 +45,43 @@ def test_infinite_and_large_arguments(M, dtype, out_dtype, activation):
     keep = torch.arange(48, device="cuda") != 2
     assert torch.equal(y[:, keep], plain[:, keep])
     w4.w4_check_device_error()
+
+
+@pytest.mark.parametrize("activation", ["silu", "gelu_tanh", "gelu"])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("M", [5, 40, 300])
+def test_activations_of_exact_sums_in_fp32(M, dtype, gated, activation):
+    """One channel of a row is not zero, scales are a power of two: every sum x (q - 8) / 8 is exact,
+    and an fp32 output is its activation alone.  With e = 2^-24: SiLU's exponential is within
+    2^-22 (2^x) + 4 e, the sum and the quotient add 2^-22 + e: below 2^-20 of the value.  The GELUs'
+    arguments are rounded, a relative 6 e, and their tails go as e^-u with u below 1 + x^2 (tanh: 1.6 |x|
+    + 0.072 |x|^3 as far as the range here, |x| <= 12; erf: x^2 / 2): within 2^-20 (1 + x^2) of the value.
+    A gated output adds one product.  Quotients by more than 2^126 are zero: |x| 2^-126."""
+    skip_without_gpu()
+    torch = torch_mod()
+    N, K = 128, 128
+    L = Layer(22, N, K, 128, True, dtype=dtype)
+    L.sc.fill_(0.125)
+    q = (L.what / Layer(22, N, K, 128, True, dtype=dtype).sc.double().repeat_interleave(128, 0).t()).round()
+    g = torch.Generator(device="cuda").manual_seed(M)
+    most = 12.0 if activation != "silu" else 80.0
+    x = ((torch.rand(M, generator=g, device="cuda") * 2 - 1) * most).to(L.dt)
+    X = torch.zeros(M, K, device="cuda").to(L.dt)
+    at = torch.randint(0, K, (M,), generator=g, device="cuda")
+    X[torch.arange(M, device="cuda"), at] = x
+    t = x.double()[:, None] * q[:, at].t() / 8
+    Y = w4.w4a16_gemm_epi(X, L.qw, L.sc, None, 128, activation=activation, gated=gated, out_dtype=torch.float32)
+    if gated:
+        t = t.view(M, -1, 2, 8)
+        t, up = t[:, :, 0].reshape(M, -1), t[:, :, 1].reshape(M, -1)
+    # (forms that keep the negative tails' digits: 1 + tanh and 1 + erf lose them in 64 bits too)
+    want = {"silu": lambda: t * torch.sigmoid(t), "gelu": lambda: 0.5 * t * torch.erfc(-t / 2 ** 0.5),
+            "gelu_tanh": lambda: t * torch.sigmoid(2 * (2 / math.pi) ** 0.5 * (t + 0.044715 * t ** 3))}[activation]()
+    rel = 2.0 ** -20 * (1 if activation == "silu" else 1 + t ** 2)
+    if gated:
+        want = want * up
+        rel = rel + 2.0 ** -24
+    bad = (Y.double() - want).abs() > rel * want.abs() + 2.0 ** -126 * (1 + t.abs()) * (1 + (up.abs() if gated else 0))
+    assert not bad.any(), (int(bad.sum()), t[bad][:4], Y[bad][:4], want[bad][:4])
+    assert t.abs().max() > 0.5 * most
