@@ -135,7 +135,9 @@ w4_status w4_quantize_pack(const void* W, w4_dtype w_dtype, int64_t N, int64_t K
  *              that may overlap on the GPU need separate workspaces.  After a call
  *              whose kernel reported W4_ERR_TIMEOUT, zero it again.
  * M == 0 is a no-op.  M <= 64 runs the bandwidth-bound decode kernel (warp MMAs,
- * split-K across the GPU), larger M the tcgen05 tensor-core kernel.
+ * split-K across the GPU), larger M the tcgen05 tensor-core kernel.  32 < M <= 64 with
+ * group_size 32 and zeros runs as two products, of 32 rows and of the rest, that read the
+ * weights once each.
  * bf16 activations with g_idx return W4_ERR_UNSUPPORTED.
  */
 w4_status w4a16_gemm(const void* X, w4_dtype act_dtype, int64_t M, int64_t N, int64_t K,

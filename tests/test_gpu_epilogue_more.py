@@ -1,11 +1,13 @@
-"""More of the products with an epilogue: activations at the ends of their range."""
+"""More of the products with an epilogue: activations at the ends of their range, and the calls
+that run as two products, in every form a call can have."""
 import math
 
+import numpy as np
 import pytest
 
 import bit_weight_only_w4_b200 as w4
-from tests.gpu_util import skip_without_gpu, torch_mod
-from tests.test_gpu_epilogue import Layer
+from tests.gpu_util import act_order, skip_without_gpu, torch_mod
+from tests.test_gpu_epilogue import Layer, check, reference
 
 pytestmark = pytest.mark.gpu
 
@@ -85,3 +87,44 @@ def test_activations_of_exact_sums_in_fp32(M, dtype, gated, activation):
     bad = (Y.double() - want).abs() > rel * want.abs() + 2.0 ** -126 * (1 + t.abs()) * (1 + (up.abs() if gated else 0))
     assert not bad.any(), (int(bad.sum()), t[bad][:4], Y[bad][:4], want[bad][:4])
     assert t.abs().max() > 0.5 * most
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("perm", [False, True])
+@pytest.mark.parametrize("M", [33, 50, 64])
+def test_two_products_strided_in_place_permuted_and_captured(M, perm, dtype):
+    """33 to 64 rows, 32-channel groups, zero points: each of the two products has to find its rows
+    of X, Y, the residual and the gathered columns."""
+    skip_without_gpu()
+    torch = torch_mod()
+    K, g = 576, 32
+    g_idx = act_order(np.random.default_rng(4), K, g) if perm else None
+    L = Layer(23, 208, K, g, dtype=dtype, g_idx=g_idx, perm=perm)
+    X = L.acts(M)
+    bias = torch.randn(208, generator=L.gen, device="cuda")
+    s_inv = torch.rand(K, generator=L.gen, device="cuda") + 0.5
+    for gated, n_out in ((False, 208), (True, 104)):
+        for out in (L.dt, torch.float32):
+            wide = torch.randn(M, n_out + 96, generator=L.gen, device="cuda").to(out)
+            keep = wide.clone()
+            Y = wide[:, 32:32 + n_out]
+            kw = dict(bias=bias, activation="silu", gated=gated, s_inv=s_inv, perm=L.perm)
+            ref = reference(L, X, bias, "silu", gated, keep[:, 32:32 + n_out], s_inv)
+            w4.w4a16_gemm_epi(X, L.qw, L.sc, L.zr, g, residual=Y, Y=Y, **kw)     # in place, rows apart
+            check(Y, ref)
+            want = Y.clone()
+            assert torch.equal(wide[:, :32], keep[:, :32]) and torch.equal(wide[:, 32 + n_out:], keep[:, 32 + n_out:])
+            far = torch.full((M, n_out + 8), 5.0, device="cuda").to(out)          # another stride than the residual's
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                w4.w4a16_gemm_epi(X, L.qw, L.sc, L.zr, g, residual=keep[:, 32:32 + n_out], Y=far[:, :n_out], **kw)
+            for _ in range(2):
+                far[:, :n_out].zero_()
+                graph.replay()
+                torch.cuda.synchronize()
+                assert torch.equal(far[:, :n_out], want) and bool((far[:, n_out:] == 5).all())
+    # the plain entry points: rows of the two products are rows of products alone
+    whole = w4.w4a16_gemm(X, L.qw, L.sc, L.zr, g, s_inv=s_inv, perm=L.perm)
+    parts = [w4.w4a16_gemm(X[a:b].contiguous(), L.qw, L.sc, L.zr, g, s_inv=s_inv, perm=L.perm) for a, b in ((0, 32), (32, M))]
+    assert torch.equal(whole, torch.cat(parts))
+    w4.w4_check_device_error()
