@@ -218,7 +218,7 @@ def _new(like, shape, dtype, stream):
     pool, whose memory no work queued on another stream still reads or writes.  The current
     stream, where the caller will read it, keeps it until its work is done."""
     if stream is None:
-        return like.new_empty(shape, dtype=dtype)
+        return like.new_empty(shape) if dtype is like.dtype else like.new_empty(shape, dtype=dtype)
     with _allocating_on(stream, like.device):
         t = like.new_empty(shape, dtype=dtype)
     t.record_stream(_torch().cuda.current_stream(like.device))
@@ -402,11 +402,8 @@ _ws_captured = {}   # (device index, stream handle): (capture, the buffer of the
 _ws_lock = threading.Lock()
 
 
-def _capture_id(index, handle, stream):
+def _capture_id(index, handle):
     """The number of the capture that records the stream's work, 0 while none does."""
-    torch = _torch()
-    if stream is None and torch._C._cuda_getDevice() == index and not torch._C._cuda_isCurrentStreamCapturing():
-        return 0
     out = ctypes.c_uint64()
     _check(_on_device(index, lib().w4_stream_capture_id, handle, ctypes.byref(out)), "w4_stream_capture_id")
     return out.value
@@ -425,8 +422,17 @@ def workspace_for(device, nbytes, stream=None):
     device = torch.device(device)
     index = torch.cuda.current_device() if device.index is None else device.index
     handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
-    capture = _capture_id(index, handle, stream)
+    return _scratch(torch, device, index, handle, nbytes, stream)
+
+
+def _scratch(torch, device, index, handle, nbytes, stream):
     key = (index, handle)
+    buf = _ws_cache.get(key)
+    # the common case, at little cost: an eager call on the current stream
+    if buf is not None and buf.numel() >= nbytes and stream is None and torch._C._cuda_getDevice() == index \
+            and not torch._C._cuda_isCurrentStreamCapturing():
+        return buf
+    capture = _capture_id(index, handle)
     with _ws_lock:
         if capture:
             owner, buf = _ws_captured.get(key, (0, None))
@@ -517,24 +523,22 @@ def w4a16_gemm(X, qweight, scales, zeros, group_size=128, g_idx=None, s_inv=None
     out_dtype = out_dtype or X.dtype
     if Y is None:
         Y = _new(X, (M, N), out_dtype, stream)
+    handle = _stream_handle(stream, dev)
     with _DeviceGuard(dev):
-        if perm is not None:
-            need = lib().w4a16_workspace_bytes_perm(M, N, K, int(group_size)) if M > 0 else 0
-        else:
-            need = w4a16_workspace_bytes(M, N, K, group_size) if M > 0 else 0
-        if workspace is None and need > 0:
-            workspace = workspace_for(dev, need, stream)
+        if workspace is None and M > 0:
+            size = lib().w4a16_workspace_bytes if perm is None else lib().w4a16_workspace_bytes_perm
+            need = _workspace_size(dev.index, size, M, N, K, int(group_size))
+            if need > 0:
+                workspace = _scratch(torch, dev, dev.index, handle, need, stream)
         ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
         if perm is not None:
             st = lib().w4a16_gemm_perm(_ptr(X), _dtype_code(X.dtype), M, N, K, _ptr(qweight), _ptr(scales),
                                        _ptr(zeros), _ptr(perm), int(group_size), _ptr(s_inv), _ptr(Y),
-                                       _dtype_code(Y.dtype), _ptr(workspace), ws_bytes,
-                                       _stream_handle(stream, dev))
+                                       _dtype_code(Y.dtype), _ptr(workspace), ws_bytes, handle)
         else:
             st = lib().w4a16_gemm(_ptr(X), _dtype_code(X.dtype), M, N, K, _ptr(qweight), _ptr(scales),
                                   _ptr(zeros), _ptr(g_idx), int(group_size), _ptr(s_inv), _ptr(Y),
-                                  _dtype_code(Y.dtype), _ptr(workspace), ws_bytes,
-                                  _stream_handle(stream, dev))
+                                  _dtype_code(Y.dtype), _ptr(workspace), ws_bytes, handle)
     _check(st, "w4a16_gemm_perm" if perm is not None else "w4a16_gemm")
     return Y
 
@@ -625,7 +629,7 @@ def w4a16_fp4_gemm(X, qweight, block_scales, tensor_scale=None, fmt="nvfp4", out
     with _DeviceGuard(dev):
         need = w4a16_fp4_workspace_bytes(M, N, K, f) if M > 0 else 0
         if workspace is None and need > 0:
-            workspace = workspace_for(dev, need, stream)
+            workspace = _scratch(torch, dev, dev.index, _stream_handle(stream, dev), need, stream)
         ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
         st = lib().w4a16_fp4_gemm(_ptr(X), _dtype_code(X.dtype), M, N, K, _ptr(qweight), _ptr(block_scales),
                                   _ptr(tensor_scale), f, _ptr(Y), _dtype_code(Y.dtype), _ptr(workspace),
@@ -681,7 +685,7 @@ def w4a16_gemm_chain(layers, workspace=None, stream=None):
     with _DeviceGuard(dev):
         need = w4a16_chain_workspace_bytes(M)
         if workspace is None and need > 0:
-            workspace = workspace_for(dev, need, stream)
+            workspace = _scratch(torch, dev, dev.index, _stream_handle(stream, dev), need, stream)
         ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
         st = lib().w4a16_gemm_chain(arr, n, M, _dtype_code(act), _dtype_code(out), _ptr(workspace),
                                     ws_bytes, _stream_handle(stream, dev))
@@ -796,16 +800,16 @@ def w4a16_gemm_epi(X, qweight, scales, zeros, group_size=128, bias=None, activat
     e = Epilogue(_ptr(bias), _ptr(residual), ldr, ldy, 0 if bias is None else _dtype_code(bias.dtype),
                  0 if residual is None else _dtype_code(residual.dtype), act, 1 if gated else 0)
     L = lib()
+    handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
     if workspace is None and M > 0:
         need = _workspace_size(index, L.w4a16_workspace_bytes if perm is None else L.w4a16_workspace_bytes_perm,
                                M, N, K, group_size)
         if need > 0:
-            workspace = workspace_for(X.device, need, stream)
+            workspace = _scratch(torch, X.device, index, handle, need, stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     st = _on_device(index, L.w4a16_gemm_epi, X.data_ptr(), _dtype_code(xt), M, N, K, qweight.data_ptr(),
                     scales.data_ptr(), _ptr(zeros), _ptr(g_idx), _ptr(perm), group_size, _ptr(s_inv), e, Y.data_ptr(),
-                    _dtype_code(yt), _ptr(workspace), ws_bytes,
-                    torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
+                    _dtype_code(yt), _ptr(workspace), ws_bytes, handle)
     if st:
         raise W4Error(st, "w4a16_gemm_epi")
     return Y

@@ -15,7 +15,9 @@ def on(monkeypatch):
     build.build()
     now = [0, 0]
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: now[0], raising=False)
-    monkeypatch.setattr(w4, "_capture_id", lambda index, handle, stream: now[1], raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_isCurrentStreamCapturing", lambda: now[1] != 0, raising=False)
+    monkeypatch.setattr(w4, "_capture_id", lambda index, handle: now[1], raising=False)
     monkeypatch.setattr(w4, "_ws_cache", {})
     monkeypatch.setattr(w4, "_ws_captured", {}, raising=False)
     monkeypatch.setattr(w4, "_workspace_size", lambda index, fn, *a: 4096)   # zeroed at the front of a capture's buffer
