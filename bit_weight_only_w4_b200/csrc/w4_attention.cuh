@@ -35,11 +35,16 @@
 // tile (540 us: a 128 x 64 product costs as much as a 128 x 128 one), and an eighth, a quarter
 // or a third of the exponentials as a polynomial on the FMA units (456, 467, 472 us); a fourth
 // warpgroup for the output beside softmax warps of 184 registers (457 us, and packed prompts
-// 187 against 173).  As it stands: 437 us, 1258 TFLOP/s.
+// 187 against 173).  As it stands: 436 us (1261 TFLOP/s) in a few calls on a cool board, 500 to 510 us
+// (1090) in a long run, which the board's power bounds.
 //
 // Two ways to share the work:
-//   items    longest first, one CTA an item; a running CTA takes the place of one that has
-//            not started (cluster launch control), so the hardware balances their lengths;
+//   items    by their place in the sequence, last ones first, one CTA an item; a running CTA takes
+//            the place of one that has not started (cluster launch control), so the hardware
+//            balances their lengths.  Under a causal mask without earlier keys that is longest
+//            first.  A sequence of few tokens over many earlier keys comes late, and its keys are
+//            not cut: 2000 tokens packed with 15 next tokens over 60,000 keys each (64/8 heads)
+//            take 820 us, in calls of their own 76 and 569;
 //   ranges   (few tokens over many keys) all key blocks of all items in one list, cut into
 //            equal runs, one a CTA: every SM reads the same number of keys whatever the
 //            sequences' lengths.  An item that a cut divides is written as partial outputs
@@ -185,7 +190,7 @@ struct Seqs {
 };
 
 // Finds items, by one warp.  The items of all sequences are taken in descending index in
-// their sequence (with causal masks, descending cost): item `idx` is at the level v with
+// their sequence (with causal masks and no earlier keys, descending cost): item `idx` is at the level v with
 // f(v) > idx >= f(v + 1), f(v) = sum_b max(0, items of b - v), found by bisection.
 struct Finder {
     Seqs seqs;       // the first 32

@@ -763,8 +763,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // The same product with an epilogue (kernels of their own: the plain product keeps its code).
-// 2048 x 28672 x 4096 with SwiGLU 567 us (the product alone 536), 2048 x 4096 x 14336 with a
-// residual 292 us (281): the drain's excess over what the two tensor-memory buffers hide.
+// 2048 x 28672 x 4096 with SwiGLU 567 to 611 us (the product alone 536 to 590 in the same runs: a
+// cool board, a long run at its power limit), 2048 x 4096 x 14336 with a residual 292 to 312 us
+// (281 to 302): the drain's excess over what the two tensor-memory buffers hide.
 template <bool BF16, int WM, int EPI>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_epi_kernel(const __grid_constant__ CUtensorMap tmap_x, const PrefillParams p, const w4e::Epilogue epi) {
