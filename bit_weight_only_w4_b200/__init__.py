@@ -417,7 +417,8 @@ def workspace_for(device, nbytes, stream=None):
     outgrown and its memory goes back to that stream's pool.  Calls that a graph capture
     records share one that belongs to the graph (allocated within the capture, its split-K slots
     zeroed by every replay), and no later call takes that one.  So graphs may be replayed beside
-    each other and beside eager calls."""
+    each other and beside eager calls (a layer sequence, w4a16_gemm_chain, wants the GPU's SMs to
+    itself all the same)."""
     torch = _torch()
     device = torch.device(device)
     index = torch.cuda.current_device() if device.index is None else device.index
@@ -647,7 +648,9 @@ def w4a16_gemm_chain(layers, workspace=None, stream=None):
     layers.  Each layer is a dict with X, qweight, scales, zeros, group_size, s_inv and Y
     (X [M,K] may be a view of an earlier layer's Y: rows may be further apart than K,
     elements must be contiguous).  Layer l+1 reads its X only after every earlier output
-    is stored.  Outputs are written into the given Y tensors; returns the list of Ys."""
+    is stored.  Outputs are written into the given Y tensors; returns the list of Ys.  The CTAs
+    of a launch wait for one another, so no other work may hold SMs meanwhile: such a wait ends
+    after the wait limit, and w4_check_device_error() reports it."""
     torch = _torch()
     n = len(layers)
     if n == 0:
